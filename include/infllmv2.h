@@ -64,7 +64,8 @@ enum {
 /* Device error word bits (infllmv2_device_error). */
 enum {
   INFLLMV2_DEVERR_WAIT_TIMEOUT = 1, /* an internal wait ran out of its time limit */
-  INFLLMV2_DEVERR_CACHE_FULL = 2    /* infllmv2_append_kv met lens[b] outside [0, Lmax) */
+  INFLLMV2_DEVERR_CACHE_FULL = 2    /* infllmv2_append_kv met lens[b] outside [0, Lmax), or
+                                       infllmv2_qk_norm_rope rows past the table or the caches */
 };
 
 enum { INFLLMV2_MODE_PREFILL = 0, INFLLMV2_MODE_DECODE = 1 };
@@ -76,7 +77,11 @@ enum {
   INFLLMV2_OP_SELECT_DECODE = 2,
   INFLLMV2_OP_ATTN_PREFILL = 3,
   INFLLMV2_OP_ATTN_DECODE = 4,
-  INFLLMV2_OP_ATTN_BACKWARD = 5
+  INFLLMV2_OP_ATTN_BACKWARD = 5,
+  INFLLMV2_OP_QK_NORM_ROPE_BACKWARD = 6,
+  INFLLMV2_OP_WINDOW_ATTN = 7,
+  INFLLMV2_OP_WINDOW_DECODE = 8,
+  INFLLMV2_OP_WINDOW_BACKWARD = 9
 };
 
 /* Problem description shared by all calls.
@@ -325,6 +330,124 @@ INFLLMV2_API int infllmv2_sparse_attn_decode_noalloc(const infllmv2_params* p, c
 INFLLMV2_API int infllmv2_append_kv(const infllmv2_params* p, const void* k_new, const void* v_new, void* k_cache,
                                     void* v_cache, int32_t* lens, int32_t Lmax, void* kc,
                                     infllmv2_stream_t stream);
+
+/* Rotation table for infllmv2_qk_norm_rope: row t holds scale * cos(t f_i) in columns
+ * 0..rot/2-1 and scale * sin(t f_i) in columns rot/2..rot-1, i = 0..rot/2-1.  The angles
+ * t f_i are formed and reduced in fp64 (a position of 10^5 leaves an fp32 angle three
+ * decimals) and each value is rounded once to fp32.
+ *   inv_freq  fp32 [rot / 2] device: the frequencies f_i
+ *   rot       rotated leading dimensions of a head: a multiple of 16, 16..128
+ *   n         rows (positions 0..n-1), 1 <= n <= INFLLMV2_MAX_SEQ_LEN
+ *   scale     multiplies cos and sin (1 for a plain rotation); finite
+ *   table     fp32 [n, rot] (output) */
+INFLLMV2_API int infllmv2_rope_table(const infllmv2_params* p, const float* inv_freq, int32_t rot, int32_t n,
+                                     float scale, float* table, infllmv2_stream_t stream);
+
+/* Norm of the queries and keys for each head and their position rotation, in one pass from
+ * the projection's rows to the layouts that the attention calls take.  For every head row
+ * x of q and k of the token at position t:
+ *   y = x / sqrt(mean(x^2) + eps) * w        (fp32; w = q_weight or k_weight)
+ *   (y_a, y_b) <- (y_a c_i - y_b s_i, y_a s_i + y_b c_i)  for the pairs i = 0..rot/2-1 with
+ *   a = i, b = i + rot/2 (interleaved = 0) or a = 2i, b = 2i + 1 (interleaved = 1), c_i and
+ *   s_i from row t of the table; dimensions rot..127 are not rotated.  Rounded once to
+ *   bf16.  v rows are moved as they are.
+ *   q, k, v    bf16 token rows: row b * Lq + r starts at (b * Lq + r) * {q,k,v}_stride elements
+ *              and holds [Hq, d] (k, v: [Hkv, d]) contiguous values; a packed projection
+ *              output [B, Lq, Hq + 2 Hkv, d] is three such views.  Strides: multiples of 8
+ *              and at least Hq * d (k, v: Hkv * d).
+ *   q_weight, k_weight  [d], fp32 (weights_fp32 != 0) or bf16, or NULL (1)
+ *   eps        finite, > 0
+ *   table      fp32 [table_rows, rot] (infllmv2_rope_table's layout)
+ *   starts     int32 [B] device or NULL (0): row r of sequence b sits at position starts[b] + r
+ *              (the tokens cached before the call)
+ *   q_lens     int32 [B] device or NULL (Lq): rows at or past q_lens[b] (clamped to [0, Lq])
+ *              are padding, neither read nor written
+ *   q_out      bf16 [B, Lq, Hq, d]
+ *   k_out, v_out  bf16 [B, Hkv, Lout, d]; at_position = 0: row r of sequence b goes to row r
+ *              (Lout >= Lq); at_position = 1: to row starts[b] + r (caches, Lout = Lmax)
+ *   lens_out   int32 [B] device or NULL: starts[b] + the sequence's rows; not starts itself
+ * A sequence whose rows leave the table (starts[b] < 0, or starts[b] + rows > table_rows) or, at
+ * position, the caches (> Lout) is left untouched (lens_out[b] = starts[b]) and sets
+ * INFLLMV2_DEVERR_CACHE_FULL in the device error word.  Outputs must not overlap inputs.
+ * No workspace. */
+INFLLMV2_API int infllmv2_qk_norm_rope(const infllmv2_params* p, const void* q, int64_t q_stride, const void* k,
+                                       int64_t k_stride, const void* v, int64_t v_stride, int32_t Lq,
+                                       const void* q_weight, const void* k_weight, int32_t weights_fp32, float eps,
+                                       const float* table, int32_t table_rows, int32_t rot, int32_t interleaved,
+                                       const int32_t* starts, const int32_t* q_lens, void* q_out, void* k_out,
+                                       void* v_out, int32_t Lout, int32_t at_position, int32_t* lens_out,
+                                       infllmv2_stream_t stream);
+
+/* Backward of infllmv2_qk_norm_rope from the attention's gradients to the projection's rows.
+ * With g = the gradient rotated back (by -angle), r = 1 / sqrt(mean(x^2) + eps):
+ *   d_w += g * x * r over every row,   dx = r (g w) - x r^3 mean(g w x).
+ * The norm is recomputed from x: nothing of the forward is kept.
+ *   q, k       the forward's inputs (with their strides), d_q bf16 [B, Lq, Hq, d], d_k and
+ *              d_v bf16 [B, Hkv, Lq, d] (fresh outputs: row r of sequence b is its row r)
+ *   dq_in, dk_in, dv_in  bf16 token rows with strides d*_stride as for the forward's inputs
+ *              (rows of padding are not written; all three may be views of one packed tensor)
+ *   d_qw, d_kw fp32 [d] gradients of the weights, or NULL
+ *   starts, q_lens, table as for the forward; a sequence that leaves the table is left
+ *              untouched, adds nothing to the weights' gradients, and sets
+ *              INFLLMV2_DEVERR_CACHE_FULL
+ *   ws         at least infllmv2_workspace_size(p, INFLLMV2_OP_QK_NORM_ROPE_BACKWARD, Lq)
+ *              bytes (contents on entry do not matter)
+ * Deterministic: the weights' gradients are summed in a fixed order. */
+INFLLMV2_API int infllmv2_qk_norm_rope_backward(
+    const infllmv2_params* p, const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* d_q,
+    const void* d_k, const void* d_v, int32_t Lq, const void* q_weight, const void* k_weight, int32_t weights_fp32,
+    float eps, const float* table, int32_t table_rows, int32_t rot, int32_t interleaved, const int32_t* starts,
+    const int32_t* q_lens, void* dq_in, int64_t dq_stride, void* dk_in, int64_t dk_stride, void* dv_in,
+    int64_t dv_stride, float* d_qw, float* d_kw, void* ws, size_t ws_bytes, infllmv2_stream_t stream);
+
+/* Sliding-window attention with a few first tokens that stay visible: the dense companion of
+ * the block-sparse calls (whose forced initial and local blocks are its block form), for the
+ * layers of a model that do not select.  The query at position t sees the keys u <= t with
+ *   u > t - window   or   u < n_sink;
+ * O = softmax(scale q K^T) V over them.  window >= the sequence length is plain causal
+ * attention.  Queries, caches and lengths as for infllmv2_sparse_attn_chunk: row r of
+ * sequence b sits at kv_lens[b] - q_lens[b] + r; a fresh prefill is q_lens = kv_lens = NULL,
+ * Lq = Lmax = L.
+ *   q          bf16 [B, Lq, Hq, d];  k, v  bf16 [B, Hkv, Lmax, d]
+ *   window     >= 1;  n_sink >= 0
+ *   o          bf16 [B, Lq, Hq, d];  lse fp32 [B, Hq, Lq] or NULL
+ *   ws         at least infllmv2_workspace_size(p, INFLLMV2_OP_WINDOW_ATTN, Lq) bytes (may be
+ *              NULL when that size is 0); contents on entry do not matter
+ * Padding rows (r >= q_lens[b]) are not written.  Cache rows that no query of the call sees
+ * may hold anything, NaN included; a key or value row that some query sees must be finite
+ * (an infinity or NaN there may reach other queries of the call that do not see it). */
+INFLLMV2_API int infllmv2_window_attn(const infllmv2_params* p, const void* q, int32_t Lq, const void* k,
+                                      const void* v, const int32_t* q_lens, const int32_t* kv_lens, int32_t Lmax,
+                                      int32_t window, int32_t n_sink, void* o, float* lse, void* ws, size_t ws_bytes,
+                                      infllmv2_stream_t stream);
+
+/* The same for one decode token per sequence, at position min(lens[b], Lmax) - 1.
+ *   q          bf16 [B, Hq, d];  k_cache, v_cache bf16 [B, Hkv, Lmax, d]
+ *   lens       int32 [B] device; a sequence with lens[b] <= 0 gets o = 0 and lse = -inf
+ *   o          bf16 [B, Hq, d];  lse fp32 [B, Hq] or NULL
+ *   ws         at least infllmv2_workspace_size(p, INFLLMV2_OP_WINDOW_DECODE, Lmax) bytes (may
+ *              be NULL when that size is 0); contents on entry do not matter.  Calls that
+ *              overlap on the GPU need a workspace each.
+ * Cache rows that the query does not see may hold anything, NaN included. */
+INFLLMV2_API int infllmv2_window_attn_decode(const infllmv2_params* p, const void* q, const void* k_cache,
+                                             const void* v_cache, const int32_t* lens, int32_t Lmax, int32_t window,
+                                             int32_t n_sink, void* o, float* lse, void* ws, size_t ws_bytes,
+                                             infllmv2_stream_t stream);
+
+/* Backward of the window attention over fresh sequences (query t at position t), with the
+ * formulas of infllmv2_sparse_attn_backward over the visible keys.
+ *   q, o, d_o  bf16 [B, L, Hq, d];  k, v bf16 [B, Hkv, L, d];  lse fp32 [B, Hq, L] (o and lse
+ *              from infllmv2_window_attn with q_lens = kv_lens = lens)
+ *   lens       int32 [B] device or NULL: sequence b holds lens[b] tokens (clamped to [0, L]);
+ *              rows at or past lens[b] are padding: not read, and their gradients not written
+ *   dq         bf16 [B, L, Hq, d];  dk, dv bf16 [B, Hkv, L, d] (outputs)
+ *   ws         at least infllmv2_workspace_size(p, INFLLMV2_OP_WINDOW_BACKWARD, L) bytes
+ * Deterministic: no atomics; a shared head's dk and dv are summed over its group inside one
+ * CTA. */
+INFLLMV2_API int infllmv2_window_attn_backward(const infllmv2_params* p, const void* q, const void* k, const void* v,
+                                               const void* o, const float* lse, const void* d_o, const int32_t* lens,
+                                               int32_t L, int32_t window, int32_t n_sink, void* dq, void* dk, void* dv,
+                                               void* ws, size_t ws_bytes, infllmv2_stream_t stream);
 
 /* Workspace bytes needed by `op` (INFLLMV2_OP_*) for sequence length L_or_Lmax, or 0
  * when the op needs none; (size_t)-1 for invalid parameters. */

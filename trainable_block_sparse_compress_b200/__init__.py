@@ -14,6 +14,9 @@ from .ops import (  # noqa: F401
     num_kernels,
     prefill,
     prefill_chunk,
+    qk_norm_rope,
+    qk_norm_rope_backward,
+    rope_table,
     select_blocks_chunk,
     sparse_attn_backward,
     sparse_attn_chunk,
@@ -22,5 +25,9 @@ from .ops import (  # noqa: F401
     sparse_attn_decode,
     sparse_attn_decode_noalloc,
     sparse_attn_prefill,
+    window_attn_backward,
+    window_attn_chunk,
+    window_attn_decode,
+    window_attn_prefill,
     workspace_size,
 )

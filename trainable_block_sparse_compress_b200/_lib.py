@@ -32,6 +32,13 @@ OP_SELECT_DECODE = 2
 OP_ATTN_PREFILL = 3
 OP_ATTN_DECODE = 4
 OP_ATTN_BACKWARD = 5
+OP_QK_NORM_ROPE_BACKWARD = 6
+OP_WINDOW_ATTN = 7
+OP_WINDOW_DECODE = 8
+OP_WINDOW_BACKWARD = 9
+
+DEVERR_WAIT_TIMEOUT = 1
+DEVERR_CACHE_FULL = 2
 
 MAX_SEQ_LEN = 262144
 NOALLOC_SCRATCH_BYTES = 8 << 20
@@ -42,6 +49,7 @@ _i32 = ctypes.c_int32
 _i64 = ctypes.c_int64
 _int = ctypes.c_int
 _sz = ctypes.c_size_t
+_f32 = ctypes.c_float
 
 
 class CParams(ctypes.Structure):
@@ -76,6 +84,16 @@ SIGNATURES = {
     "infllmv2_sparse_attn_decode_noalloc": (_int, [_P, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp]),
     "infllmv2_append_kv": (_int, [_P, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp]),
     "infllmv2_decode_step": (_int, [_P, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp]),
+    "infllmv2_rope_table": (_int, [_P, _vp, _i32, _i32, _f32, _vp, _vp]),
+    "infllmv2_qk_norm_rope": (_int, [_P, _vp, _i64, _vp, _i64, _vp, _i64, _i32, _vp, _vp, _i32, _f32, _vp, _i32, _i32,
+                                     _i32, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _vp]),
+    "infllmv2_qk_norm_rope_backward": (_int, [_P, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _f32, _vp,
+                                              _i32, _i32, _i32, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp,
+                                              _vp, _sz, _vp]),
+    "infllmv2_window_attn": (_int, [_P, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _sz, _vp]),
+    "infllmv2_window_attn_decode": (_int, [_P, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _sz, _vp]),
+    "infllmv2_window_attn_backward": (_int, [_P, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp,
+                                             _vp, _sz, _vp]),
     "infllmv2_workspace_size": (_sz, [_P, _int, _i32]),
     "infllmv2_check_params": (_int, [_P]),
     "infllmv2_status_string": (ctypes.c_char_p, [_int]),

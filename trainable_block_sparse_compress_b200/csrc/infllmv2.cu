@@ -23,16 +23,18 @@
 #include "common.cuh"
 #include "compress.cuh"
 #include "decode_step.cuh"
+#include "norm_rope.cuh"
 #include "select_decode.cuh"
 #include "select_prefill.cuh"
 #include "select_prefill_tc.cuh"
 #include "topk.cuh"
+#include "window.cuh"
 
 using namespace infllmv2;
 
 namespace {
 
-constexpr int kVersion = 200;  // 0.2.0
+constexpr int kVersion = 300;  // 0.3.0
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -302,9 +304,100 @@ size_t ws_size(const infllmv2_params* p, int op, int32_t L) {
       const size_t rows = static_cast<size_t>(p->batch) * p->num_kv_heads * d.n_splits * kGroupRows;
       return rows * kHeadDim * sizeof(float) + rows * sizeof(float);
     }
+    case INFLLMV2_OP_QK_NORM_ROPE_BACKWARD:
+      return static_cast<size_t>(kNrMaxParts) * 2 * kHeadDim * sizeof(float);
+    case INFLLMV2_OP_WINDOW_ATTN:
+    case INFLLMV2_OP_WINDOW_DECODE:
+    case INFLLMV2_OP_WINDOW_BACKWARD:
+      return 0;
     default:
       return static_cast<size_t>(-1);
   }
+}
+
+int check_chunk(int32_t Lq, const int32_t* q_lens, const int32_t* kv_lens, int32_t Lmax);
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Shared checks and parameters of the norm-and-rotation calls.
+int norm_rope_args(const infllmv2_params* p, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                   int32_t Lq, const void* qw, const void* kw, int32_t weights_fp32, float eps, const float* table,
+                   int32_t table_rows, int32_t rot, int32_t interleaved, const int32_t* starts,
+                   const int32_t* q_lens, NormRopeParams& a) {
+  int st = check_params(p);
+  if (st != INFLLMV2_OK) return st;
+  if ((st = check_len(Lq)) != INFLLMV2_OK || (st = check_len(table_rows)) != INFLLMV2_OK) return st;
+  if (!q || !k || !table || !aligned16(q) || !aligned16(k) || !aligned16(table) || !aligned16(qw) || !aligned16(kw) ||
+      !aligned4(starts) || !aligned4(q_lens))
+    return INFLLMV2_ERR_INVALID_ARG;
+  const int64_t qn = static_cast<int64_t>(p->num_q_heads) * kHeadDim, kn = static_cast<int64_t>(p->num_kv_heads) * kHeadDim;
+  if (q_stride < qn || k_stride < kn || q_stride % 8 != 0 || k_stride % 8 != 0) return INFLLMV2_ERR_INVALID_ARG;
+  if (!(eps > 0.f) || !std::isfinite(eps)) return INFLLMV2_ERR_INVALID_ARG;
+  if (rot < 16 || rot > kHeadDim || rot % 16 != 0) return INFLLMV2_ERR_INVALID_ARG;
+  if ((interleaved != 0 && interleaved != 1) || (weights_fp32 != 0 && weights_fp32 != 1)) return INFLLMV2_ERR_INVALID_ARG;
+  a = {};
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.qw = qw;
+  a.kw = kw;
+  a.table = table;
+  a.starts = starts;
+  a.q_lens = q_lens;
+  a.B = p->batch;
+  a.Lq = Lq;
+  a.Hq = p->num_q_heads;
+  a.Hkv = p->num_kv_heads;
+  a.weights_fp32 = weights_fp32;
+  a.table_rows = table_rows;
+  a.rot = rot;
+  a.eps = eps;
+  return INFLLMV2_OK;
+}
+
+// Heads of one item and CTAs of the launch: up to 12 heads a half-warp (the table row and the
+// weights are loaded once for them), fewer while the items would leave half-warps of the GPU
+// without work.
+unsigned norm_rope_grid(NormRopeParams& a, int ctas_per_sm) {
+  const long long tokens = static_cast<long long>(a.B) * a.Lq, room = static_cast<long long>(ctas_per_sm) * num_sms();
+  const int H = a.Hq + 2 * a.Hkv;
+  a.chunks = (H + 11) / 12;
+  while (a.chunks < H && tokens * a.chunks * 2 <= room * kNrHalves) a.chunks = std::min(H, 2 * a.chunks);
+  a.heads_per_item = (H + a.chunks - 1) / a.chunks;
+  a.chunks = (H + a.heads_per_item - 1) / a.heads_per_item;
+  return static_cast<unsigned>(std::min<long long>((tokens * a.chunks + kNrHalves - 1) / kNrHalves, room));
+}
+
+// Shared checks and parameters of the window attention calls.
+int window_args(const infllmv2_params* p, const void* q, int32_t Lq, const void* k, const void* v,
+                const int32_t* q_lens, const int32_t* kv_lens, int32_t Lmax, int32_t window, int32_t n_sink,
+                WinParams& a) {
+  int st = check_params(p);
+  if (st != INFLLMV2_OK) return st;
+  if ((st = check_chunk(Lq, q_lens, kv_lens, Lmax)) != INFLLMV2_OK) return st;
+  if (!q || !k || !v || !aligned16(q) || !aligned16(k) || !aligned16(v)) return INFLLMV2_ERR_INVALID_ARG;
+  if (window < 1 || n_sink < 0) return INFLLMV2_ERR_INVALID_ARG;
+  if (static_cast<uint64_t>(p->batch) * Lq * p->num_q_heads > 0x7fffffffULL ||
+      static_cast<uint64_t>(p->batch) * p->num_kv_heads * Lmax > 0x7fffffffULL)
+    return INFLLMV2_ERR_UNSUPPORTED;  // 32-bit row numbers
+  a = {};
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.k = static_cast<const __nv_bfloat16*>(k);
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  a.q_lens = q_lens;
+  a.kv_lens = kv_lens;
+  a.B = p->batch;
+  a.Hq = p->num_q_heads;
+  a.Hkv = p->num_kv_heads;
+  a.G = p->num_q_heads / p->num_kv_heads;
+  a.Lq = Lq;
+  a.Lmax = Lmax;
+  a.window = window;
+  a.n_sink = n_sink;
+  a.scale_log2 = scale_log2(p);
+  a.scale = a.scale_log2 / 1.4426950408889634f;
+  return INFLLMV2_OK;
 }
 
 // Chunk arguments: Lq and Lmax in [1, INFLLMV2_MAX_SEQ_LEN], Lq <= Lmax, length arrays
@@ -843,6 +936,150 @@ int infllmv2_decode_step(const infllmv2_params* p, const void* q, const void* k_
   if (grid > 0x7fffffffLL) return INFLLMV2_ERR_UNSUPPORTED;
   return launch_cluster(decode_step_kernel, static_cast<unsigned>(grid), C, kSdThreads, decode_step_smem_bytes(),
                         reinterpret_cast<cudaStream_t>(stream), true, tm_kc, tq, tk, tv, P);
+}
+
+int infllmv2_rope_table(const infllmv2_params* p, const float* inv_freq, int32_t rot, int32_t n, float scale,
+                        float* table, infllmv2_stream_t stream) {
+  int st = check_params(p);
+  if (st != INFLLMV2_OK) return st;
+  if ((st = check_len(n)) != INFLLMV2_OK) return st;
+  if (!inv_freq || !table || !aligned4(inv_freq) || !aligned16(table)) return INFLLMV2_ERR_INVALID_ARG;
+  if (rot < 16 || rot > kHeadDim || rot % 16 != 0 || !std::isfinite(scale)) return INFLLMV2_ERR_INVALID_ARG;
+  const long long ctas = (static_cast<long long>(n) * (rot / 2) + 255) / 256;
+  rope_table_kernel<<<static_cast<unsigned>(std::min<long long>(ctas, 8LL * num_sms())), 256, 0,
+                      reinterpret_cast<cudaStream_t>(stream)>>>(inv_freq, rot, n, scale, table);
+  return launch_status();
+}
+
+int infllmv2_qk_norm_rope(const infllmv2_params* p, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                          const void* v, int64_t v_stride, int32_t Lq, const void* q_weight, const void* k_weight,
+                          int32_t weights_fp32, float eps, const float* table, int32_t table_rows, int32_t rot,
+                          int32_t interleaved, const int32_t* starts, const int32_t* q_lens, void* q_out, void* k_out,
+                          void* v_out, int32_t Lout, int32_t at_position, int32_t* lens_out,
+                          infllmv2_stream_t stream) {
+  NormRopeParams a;
+  int st = norm_rope_args(p, q, q_stride, k, k_stride, Lq, q_weight, k_weight, weights_fp32, eps, table, table_rows,
+                          rot, interleaved, starts, q_lens, a);
+  if (st != INFLLMV2_OK) return st;
+  if ((st = check_len(Lout)) != INFLLMV2_OK) return st;
+  if (!v || !q_out || !k_out || !v_out || !aligned16(v) || !aligned16(q_out) || !aligned16(k_out) ||
+      !aligned16(v_out) || !aligned4(lens_out) || (lens_out != nullptr && lens_out == starts))
+    return INFLLMV2_ERR_INVALID_ARG;
+  if (v_stride < static_cast<int64_t>(p->num_kv_heads) * kHeadDim || v_stride % 8 != 0) return INFLLMV2_ERR_INVALID_ARG;
+  if ((at_position != 0 && at_position != 1) || (at_position == 0 && Lout < Lq)) return INFLLMV2_ERR_INVALID_ARG;
+  a.v = static_cast<const __nv_bfloat16*>(v);
+  a.v_stride = v_stride;
+  a.q_out = static_cast<__nv_bfloat16*>(q_out);
+  a.k_out = static_cast<__nv_bfloat16*>(k_out);
+  a.v_out = static_cast<__nv_bfloat16*>(v_out);
+  a.Lout = Lout;
+  a.at_position = at_position;
+  a.lens_out = lens_out;
+  const unsigned grid = norm_rope_grid(a, 4);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (interleaved)
+    qk_norm_rope_kernel<true><<<grid, kNrThreads, 0, s>>>(a);
+  else
+    qk_norm_rope_kernel<false><<<grid, kNrThreads, 0, s>>>(a);
+  return launch_status();
+}
+
+int infllmv2_qk_norm_rope_backward(const infllmv2_params* p, const void* q, int64_t q_stride, const void* k,
+                                   int64_t k_stride, const void* d_q, const void* d_k, const void* d_v, int32_t Lq,
+                                   const void* q_weight, const void* k_weight, int32_t weights_fp32, float eps,
+                                   const float* table, int32_t table_rows, int32_t rot, int32_t interleaved,
+                                   const int32_t* starts, const int32_t* q_lens, void* dq_in, int64_t dq_stride,
+                                   void* dk_in, int64_t dk_stride, void* dv_in, int64_t dv_stride, float* d_qw,
+                                   float* d_kw, void* ws, size_t ws_bytes, infllmv2_stream_t stream) {
+  NormRopeParams a;
+  int st = norm_rope_args(p, q, q_stride, k, k_stride, Lq, q_weight, k_weight, weights_fp32, eps, table, table_rows,
+                          rot, interleaved, starts, q_lens, a);
+  if (st != INFLLMV2_OK) return st;
+  if (!d_q || !d_k || !d_v || !dq_in || !dk_in || !dv_in || !aligned16(d_q) || !aligned16(d_k) || !aligned16(d_v) ||
+      !aligned16(dq_in) || !aligned16(dk_in) || !aligned16(dv_in) || !aligned4(d_qw) || !aligned4(d_kw))
+    return INFLLMV2_ERR_INVALID_ARG;
+  const int64_t kn = static_cast<int64_t>(p->num_kv_heads) * kHeadDim;
+  if (dq_stride < static_cast<int64_t>(p->num_q_heads) * kHeadDim || dk_stride < kn || dv_stride < kn ||
+      dq_stride % 8 != 0 || dk_stride % 8 != 0 || dv_stride % 8 != 0)
+    return INFLLMV2_ERR_INVALID_ARG;
+  if (ws == nullptr || !aligned16(ws) || ws_bytes < ws_size(p, INFLLMV2_OP_QK_NORM_ROPE_BACKWARD, Lq))
+    return INFLLMV2_ERR_WORKSPACE;
+  a.dq = static_cast<const __nv_bfloat16*>(d_q);
+  a.dk = static_cast<const __nv_bfloat16*>(d_k);
+  a.dv = static_cast<const __nv_bfloat16*>(d_v);
+  a.q_out = static_cast<__nv_bfloat16*>(dq_in);
+  a.k_out = static_cast<__nv_bfloat16*>(dk_in);
+  a.v_out = static_cast<__nv_bfloat16*>(dv_in);
+  a.dq_stride = dq_stride;
+  a.dk_stride = dk_stride;
+  a.dv_stride = dv_stride;
+  a.part = static_cast<float*>(ws);
+  const unsigned grid = std::min<unsigned>(norm_rope_grid(a, 4), kNrMaxParts);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (interleaved)
+    qk_norm_rope_bwd_kernel<true><<<grid, kNrThreads, 0, s>>>(a);
+  else
+    qk_norm_rope_bwd_kernel<false><<<grid, kNrThreads, 0, s>>>(a);
+  if ((st = launch_status()) != INFLLMV2_OK) return st;
+  if (d_qw || d_kw) qk_norm_rope_bwd_weights_kernel<<<8, 1024, 0, s>>>(a.part, static_cast<int>(grid), d_qw, d_kw);
+  return launch_status();
+}
+
+int infllmv2_window_attn(const infllmv2_params* p, const void* q, int32_t Lq, const void* k, const void* v,
+                         const int32_t* q_lens, const int32_t* kv_lens, int32_t Lmax, int32_t window, int32_t n_sink,
+                         void* o, float* lse, void* ws, size_t ws_bytes, infllmv2_stream_t stream) {
+  WinParams a;
+  int st = window_args(p, q, Lq, k, v, q_lens, kv_lens, Lmax, window, n_sink, a);
+  if (st != INFLLMV2_OK) return st;
+  if (!o || !aligned16(o) || !aligned4(lse)) return INFLLMV2_ERR_INVALID_ARG;
+  const size_t need = ws_size(p, INFLLMV2_OP_WINDOW_ATTN, Lq);
+  if (need > 0 && (ws == nullptr || ws_bytes < need || !aligned16(ws))) return INFLLMV2_ERR_WORKSPACE;
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.lse = lse;
+  const long long rows = static_cast<long long>(a.B) * a.Lq * a.Hq;
+  window_rows_kernel<<<static_cast<unsigned>((rows + 3) / 4), 128, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a, 0);
+  return launch_status();
+}
+
+int infllmv2_window_attn_decode(const infllmv2_params* p, const void* q, const void* k_cache, const void* v_cache,
+                                const int32_t* lens, int32_t Lmax, int32_t window, int32_t n_sink, void* o, float* lse,
+                                void* ws, size_t ws_bytes, infllmv2_stream_t stream) {
+  WinParams a;
+  int st = window_args(p, q, 1, k_cache, v_cache, nullptr, lens, Lmax, window, n_sink, a);
+  if (st != INFLLMV2_OK) return st;
+  if (!lens || !o || !aligned16(o) || !aligned4(lse)) return INFLLMV2_ERR_INVALID_ARG;
+  const size_t need = ws_size(p, INFLLMV2_OP_WINDOW_DECODE, Lmax);
+  if (need > 0 && (ws == nullptr || ws_bytes < need || !aligned16(ws))) return INFLLMV2_ERR_WORKSPACE;
+  a.o = static_cast<__nv_bfloat16*>(o);
+  a.lse = lse;
+  const long long rows = static_cast<long long>(a.B) * a.Hq;
+  window_rows_kernel<<<static_cast<unsigned>((rows + 3) / 4), 128, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a, 1);
+  return launch_status();
+}
+
+int infllmv2_window_attn_backward(const infllmv2_params* p, const void* q, const void* k, const void* v, const void* o,
+                                  const float* lse, const void* d_o, const int32_t* lens, int32_t L, int32_t window,
+                                  int32_t n_sink, void* dq, void* dk, void* dv, void* ws, size_t ws_bytes,
+                                  infllmv2_stream_t stream) {
+  WinParams a;
+  int st = window_args(p, q, L, k, v, lens, lens, L, window, n_sink, a);
+  if (st != INFLLMV2_OK) return st;
+  if (!o || !lse || !d_o || !dq || !dk || !dv || !aligned16(o) || !aligned16(d_o) || !aligned16(dq) ||
+      !aligned16(dk) || !aligned16(dv) || !aligned4(lse))
+    return INFLLMV2_ERR_INVALID_ARG;
+  const size_t need = ws_size(p, INFLLMV2_OP_WINDOW_BACKWARD, L);
+  if (need > 0 && (ws == nullptr || ws_bytes < need || !aligned16(ws))) return INFLLMV2_ERR_WORKSPACE;
+  a.o_in = static_cast<const __nv_bfloat16*>(o);
+  a.lse = const_cast<float*>(lse);
+  a.d_o = static_cast<const __nv_bfloat16*>(d_o);
+  a.dq = static_cast<__nv_bfloat16*>(dq);
+  a.dk = static_cast<__nv_bfloat16*>(dk);
+  a.dv = static_cast<__nv_bfloat16*>(dv);
+  const long long rows = static_cast<long long>(a.B) * a.Lq * a.Hq, keys = static_cast<long long>(a.B) * a.Lq * a.Hkv;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  window_dq_rows_kernel<<<static_cast<unsigned>((rows + 3) / 4), 128, 0, s>>>(a);
+  window_dkdv_rows_kernel<<<static_cast<unsigned>((keys + 3) / 4), 128, 0, s>>>(a);
+  return launch_status();
 }
 
 }  // extern "C"

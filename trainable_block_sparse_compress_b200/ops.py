@@ -304,6 +304,248 @@ def append_kv(p: Params, k_new: torch.Tensor, v_new: torch.Tensor, k_cache: torc
     _lib.check("infllmv2_append_kv", st)
 
 
+def rope_table(p: Params, inv_freq: torch.Tensor, n: int, scale: float = 1.0,
+               out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Rotation table for positions 0..n-1: inv_freq fp32 [rot / 2] -> fp32 [n, rot], row t =
+    scale cos(t f_i), then scale sin(t f_i), with the angles in fp64."""
+    _need(inv_freq, "inv_freq", torch.float32)
+    rot = 2 * inv_freq.numel()
+    if out is None:
+        out = torch.empty((n, rot), dtype=torch.float32, device=inv_freq.device)
+    _need(out, "table", torch.float32, (n, rot))
+    st = _lib.load().infllmv2_rope_table(ctypes.byref(p.c()), _ptr(inv_freq), rot, n, scale, _ptr(out), _stream())
+    _lib.check("infllmv2_rope_table", st)
+    return out
+
+
+def _need_tokens(t: torch.Tensor, name: str, B: int, L: int, H: int, d: int) -> int:
+    """Token rows [B, L, H, d] with contiguous [H, d] and one stride between consecutive tokens
+    (a slice of a packed projection output is such a view).  Returns that stride."""
+    if t.dim() != 4:
+        raise ValueError(f"{name} must have 4 dimensions, got {t.dim()}")
+    _need(t[:1, :1], name, torch.bfloat16)  # device and dtype; heads contiguous
+    if tuple(t.shape) != (B, L, H, d):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(B, L, H, d)}")
+    # a stride over an axis of length 1 says nothing
+    if L > 1:
+        stride = t.stride(1)
+    elif B > 1:
+        stride = t.stride(0)
+    else:
+        stride = H * d
+    if B > 1 and t.stride(0) != L * stride:
+        raise ValueError(f"{name} must have one stride between consecutive tokens, got {t.stride()}")
+    return stride
+
+
+def _norm_weights(p: Params, q_weight, k_weight) -> int:
+    """Checks the norm weights ([d], both fp32 or both bf16, each may be None); 1 when fp32."""
+    dtypes = {w.dtype for w in (q_weight, k_weight) if w is not None}
+    if len(dtypes) > 1:
+        raise ValueError("q_weight and k_weight must have one dtype")
+    dt = dtypes.pop() if dtypes else torch.bfloat16
+    if dt not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"q_weight and k_weight must be torch.float32 or torch.bfloat16, got {dt}")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _need(w, name, dt, (p.head_dim,))
+    return 1 if dt == torch.float32 else 0
+
+
+def qk_norm_rope(p: Params, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor,
+                 q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                 eps: float = 1e-6, interleaved: bool = False, starts: Optional[torch.Tensor] = None,
+                 q_lens: Optional[torch.Tensor] = None, k_cache: Optional[torch.Tensor] = None,
+                 v_cache: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                 k_out: Optional[torch.Tensor] = None, v_out: Optional[torch.Tensor] = None,
+                 lens_out: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Per-head RMS norm of q and k and their position rotation, from the projection's rows to
+    the attention's layouts.  q bf16 [B, Lq, Hq, d], k, v [B, Lq, Hkv, d] (views of one packed
+    tensor allowed: only the token stride is free); table fp32 [n, rot] (rope_table); weights
+    [d], fp32 or bf16, or None.  Row r of sequence b sits at position starts[b] + r (None: r);
+    rows at or past q_lens[b] are padding.  Returns q [B, Lq, Hq, d] and k, v: with k_cache and
+    v_cache [B, Hkv, Lmax, d], the caches with the rows written at their positions; otherwise
+    [B, Hkv, Lq, d] (with Lq = 1, q[:, 0], k[:, :, 0] and v[:, :, 0] are what decode_step
+    takes).  lens_out int32 [B], when given, receives starts[b] + the sequence's rows."""
+    B, Lq = q.shape[:2]
+    qs = _need_tokens(q, "q", p.batch, Lq, p.num_q_heads, p.head_dim)
+    ks = _need_tokens(k, "k", p.batch, Lq, p.num_kv_heads, p.head_dim)
+    vs = _need_tokens(v, "v", p.batch, Lq, p.num_kv_heads, p.head_dim)
+    _need(table, "table", torch.float32)
+    n, rot = table.shape
+    wf = _norm_weights(p, q_weight, k_weight)
+    for t, name in ((starts, "starts"), (q_lens, "q_lens"), (lens_out, "lens_out")):
+        if t is not None:
+            _need(t, name, torch.int32, (p.batch,))
+    if (k_cache is None) != (v_cache is None):
+        raise ValueError("k_cache and v_cache go together")
+    if q_out is None:
+        q_out = torch.empty((B, Lq, p.num_q_heads, p.head_dim), dtype=torch.bfloat16, device=q.device)
+    _need(q_out, "q_out", torch.bfloat16, (B, Lq, p.num_q_heads, p.head_dim))
+    if k_cache is not None:
+        if k_out is not None or v_out is not None:
+            raise ValueError("k_out and v_out are for fresh outputs, without caches")
+        k_out, v_out, Lout = k_cache, v_cache, k_cache.shape[2]
+    else:
+        Lout = Lq
+        if k_out is None:
+            k_out = torch.empty((B, p.num_kv_heads, Lq, p.head_dim), dtype=torch.bfloat16, device=q.device)
+        if v_out is None:
+            v_out = torch.empty_like(k_out)
+    for t, name in ((k_out, "k_cache" if k_cache is not None else "k_out"),
+                    (v_out, "v_cache" if k_cache is not None else "v_out")):
+        _need(t, name, torch.bfloat16, (B, p.num_kv_heads, Lout, p.head_dim))
+    st = _lib.load().infllmv2_qk_norm_rope(ctypes.byref(p.c()), _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, Lq,
+                                           _ptr(q_weight), _ptr(k_weight), wf, eps, _ptr(table), n, rot,
+                                           int(interleaved), _ptr(starts), _ptr(q_lens), _ptr(q_out), _ptr(k_out),
+                                           _ptr(v_out), Lout, int(k_cache is not None), _ptr(lens_out), _stream())
+    _lib.check("infllmv2_qk_norm_rope", st)
+    return q_out, k_out, v_out
+
+
+def qk_norm_rope_backward(p: Params, q: torch.Tensor, k: torch.Tensor, d_q: torch.Tensor, d_k: torch.Tensor,
+                          d_v: torch.Tensor, table: torch.Tensor, q_weight: Optional[torch.Tensor] = None,
+                          k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, interleaved: bool = False,
+                          starts: Optional[torch.Tensor] = None, q_lens: Optional[torch.Tensor] = None,
+                          out: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None):
+    """Gradients of qk_norm_rope's inputs: q, k as given to it, d_q bf16 [B, Lq, Hq, d], d_k, d_v
+    [B, Hkv, Lq, d] (the layouts sparse_attn_backward and window_attn_backward return).  Returns
+    (dq, dk, dv, d_qw, d_kw): token rows [B, Lq, H, d], views of one packed tensor
+    [B, Lq, Hq + 2 Hkv, d] (`out`, allocated when None; rows of padding are not written), and the
+    weights' gradients, fp32 [d] (None for a weight that is None)."""
+    B, Lq = q.shape[:2]
+    Hq, Hkv, d = p.num_q_heads, p.num_kv_heads, p.head_dim
+    qs = _need_tokens(q, "q", p.batch, Lq, Hq, d)
+    ks = _need_tokens(k, "k", p.batch, Lq, Hkv, d)
+    _need(d_q, "d_q", torch.bfloat16, (B, Lq, Hq, d))
+    _need(d_k, "d_k", torch.bfloat16, (B, Hkv, Lq, d))
+    _need(d_v, "d_v", torch.bfloat16, (B, Hkv, Lq, d))
+    _need(table, "table", torch.float32)
+    n, rot = table.shape
+    wf = _norm_weights(p, q_weight, k_weight)
+    for t, name in ((starts, "starts"), (q_lens, "q_lens")):
+        if t is not None:
+            _need(t, name, torch.int32, (p.batch,))
+    if out is None:
+        out = torch.empty((B, Lq, Hq + 2 * Hkv, d), dtype=torch.bfloat16, device=q.device)
+    _need(out, "out", torch.bfloat16, (B, Lq, Hq + 2 * Hkv, d))
+    dq, dk, dv = out[:, :, :Hq], out[:, :, Hq:Hq + Hkv], out[:, :, Hq + Hkv:]
+    d_qw = None if q_weight is None else torch.empty(d, dtype=torch.float32, device=q.device)
+    d_kw = None if k_weight is None else torch.empty(d, dtype=torch.float32, device=q.device)
+    ws = _workspace(p, _lib.OP_QK_NORM_ROPE_BACKWARD, Lq, ws, q.device)
+    nbytes = ws.numel() * ws.element_size()
+    rs = (Hq + 2 * Hkv) * d
+    st = _lib.load().infllmv2_qk_norm_rope_backward(
+        ctypes.byref(p.c()), _ptr(q), qs, _ptr(k), ks, _ptr(d_q), _ptr(d_k), _ptr(d_v), Lq, _ptr(q_weight),
+        _ptr(k_weight), wf, eps, _ptr(table), n, rot, int(interleaved), _ptr(starts), _ptr(q_lens), _ptr(dq), rs,
+        _ptr(dk), rs, _ptr(dv), rs, _ptr(d_qw), _ptr(d_kw), _ptr(ws), nbytes, _stream())
+    _lib.check("infllmv2_qk_norm_rope_backward", st)
+    return dq, dk, dv, d_qw, d_kw
+
+
+def window_attn_chunk(p: Params, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int, n_sink: int = 0,
+                      q_lens: Optional[torch.Tensor] = None, kv_lens: Optional[torch.Tensor] = None,
+                      out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                      want_lse: bool = True,
+                      ws: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Sliding-window attention of a chunk of queries (as sparse_attn_chunk: rows 0..q_lens[b]-1
+    are the last q_lens[b] of kv_lens[b] cached tokens) over caches k, v bf16 [B, Hkv, Lmax, d]:
+    the query at position t sees the keys u <= t with u > t - window or u < n_sink.  O bf16
+    [B, Lq, Hq, d], lse fp32 [B, Hq, Lq] (padding rows not written)."""
+    B, Lq, Hq, d = q.shape
+    Lmax = k.shape[2]
+    _need(q, "q", torch.bfloat16, (p.batch, Lq, p.num_q_heads, p.head_dim))
+    _need(k, "k", torch.bfloat16, (p.batch, p.num_kv_heads, Lmax, p.head_dim))
+    _need(v, "v", torch.bfloat16, (p.batch, p.num_kv_heads, Lmax, p.head_dim))
+    for t, name in ((q_lens, "q_lens"), (kv_lens, "kv_lens")):
+        if t is not None:
+            _need(t, name, torch.int32, (p.batch,))
+    if out is None:
+        out = torch.empty_like(q)
+    _need(out, "o", torch.bfloat16, tuple(q.shape))
+    if want_lse and lse is None:
+        lse = torch.empty((B, Hq, Lq), dtype=torch.float32, device=q.device)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (B, Hq, Lq))
+    ws = _workspace(p, _lib.OP_WINDOW_ATTN, Lq, ws, q.device)
+    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
+    st = _lib.load().infllmv2_window_attn(ctypes.byref(p.c()), _ptr(q), Lq, _ptr(k), _ptr(v), _ptr(q_lens),
+                                          _ptr(kv_lens), Lmax, window, n_sink, _ptr(out), _ptr(lse), _ptr(ws), nbytes,
+                                          _stream())
+    _lib.check("infllmv2_window_attn", st)
+    return out, lse
+
+
+def window_attn_prefill(p: Params, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int, n_sink: int = 0,
+                        out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                        want_lse: bool = True,
+                        ws: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Sliding-window attention of fresh sequences: q bf16 [B, L, Hq, d], k, v [B, Hkv, L, d] ->
+    O [B, L, Hq, d], lse fp32 [B, Hq, L].  window >= L is plain causal attention.  For a padded
+    batch use window_attn_chunk with q_lens = kv_lens."""
+    if k.shape[2] != q.shape[1]:
+        raise ValueError(f"k holds {k.shape[2]} tokens, q {q.shape[1]}")
+    return window_attn_chunk(p, q, k, v, window, n_sink, out=out, lse=lse, want_lse=want_lse, ws=ws)
+
+
+def window_attn_decode(p: Params, q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, lens: torch.Tensor,
+                       window: int, n_sink: int = 0, out: Optional[torch.Tensor] = None,
+                       lse: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                       want_lse: bool = True) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Sliding-window attention of one token per sequence at position lens[b]-1: q bf16
+    [B, Hq, d], caches [B, Hkv, Lmax, d] -> O [B, Hq, d], lse fp32 [B, Hq] (0 and -inf for an
+    empty sequence)."""
+    Lmax = k_cache.shape[2]
+    _need(q, "q", torch.bfloat16, (p.batch, p.num_q_heads, p.head_dim))
+    _need(k_cache, "k_cache", torch.bfloat16, (p.batch, p.num_kv_heads, Lmax, p.head_dim))
+    _need(v_cache, "v_cache", torch.bfloat16, (p.batch, p.num_kv_heads, Lmax, p.head_dim))
+    _need(lens, "lens", torch.int32, (p.batch,))
+    if out is None:
+        out = torch.empty_like(q)
+    _need(out, "o", torch.bfloat16, tuple(q.shape))
+    if want_lse and lse is None:
+        lse = torch.empty((p.batch, p.num_q_heads), dtype=torch.float32, device=q.device)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (p.batch, p.num_q_heads))
+    ws = _workspace(p, _lib.OP_WINDOW_DECODE, Lmax, ws, q.device)
+    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
+    st = _lib.load().infllmv2_window_attn_decode(ctypes.byref(p.c()), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                                 _ptr(lens), Lmax, window, n_sink, _ptr(out), _ptr(lse), _ptr(ws),
+                                                 nbytes, _stream())
+    _lib.check("infllmv2_window_attn_decode", st)
+    return out, lse
+
+
+def window_attn_backward(p: Params, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
+                         lse: torch.Tensor, d_o: torch.Tensor, window: int, n_sink: int = 0,
+                         lens: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                         dq: Optional[torch.Tensor] = None, dk: Optional[torch.Tensor] = None,
+                         dv: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Gradients of the window attention over fresh sequences of lens[b] tokens (None: L): q, o,
+    d_o bf16 [B, L, Hq, d], k, v bf16 [B, Hkv, L, d], lse fp32 [B, Hq, L] from the forward ->
+    dq [B, L, Hq, d], dk, dv [B, Hkv, L, d] (bf16; rows of padding are not written)."""
+    B, L, Hq, d = q.shape
+    for t, name in ((q, "q"), (o, "o"), (d_o, "d_o")):
+        _need(t, name, torch.bfloat16, (p.batch, L, p.num_q_heads, p.head_dim))
+    for t, name in ((k, "k"), (v, "v")):
+        _need(t, name, torch.bfloat16, (p.batch, p.num_kv_heads, L, p.head_dim))
+    _need(lse, "lse", torch.float32, (p.batch, p.num_q_heads, L))
+    if lens is not None:
+        _need(lens, "lens", torch.int32, (p.batch,))
+    dq = torch.empty_like(q) if dq is None else dq
+    dk = torch.empty_like(k) if dk is None else dk
+    dv = torch.empty_like(v) if dv is None else dv
+    for t, ref, name in ((dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv")):
+        _need(t, name, torch.bfloat16, tuple(ref.shape))
+    ws = _workspace(p, _lib.OP_WINDOW_BACKWARD, L, ws, q.device)
+    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
+    st = _lib.load().infllmv2_window_attn_backward(ctypes.byref(p.c()), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse),
+                                                   _ptr(d_o), _ptr(lens), L, window, n_sink, _ptr(dq), _ptr(dk),
+                                                   _ptr(dv), _ptr(ws), nbytes, _stream())
+    _lib.check("infllmv2_window_attn_backward", st)
+    return dq, dk, dv
+
+
 def device_error(clear: bool = True) -> int:
     v = int(_lib.load().infllmv2_device_error(1 if clear else 0))
     if v < 0:
