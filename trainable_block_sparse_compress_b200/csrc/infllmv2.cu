@@ -29,6 +29,7 @@
 #include "select_prefill_tc.cuh"
 #include "topk.cuh"
 #include "window.cuh"
+#include "window_tc.cuh"
 
 using namespace infllmv2;
 
@@ -111,6 +112,21 @@ bool make_q_map_3d(CUtensorMap* m, const void* q, uint64_t tokens, uint64_t head
   cuuint32_t box[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(128 / G)};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+// 3-D view [sequence x kv-head, tokens, 128] of keys or values, box {64 columns, 64 tokens, 1};
+// rows at or past `rows` (of Lmax) read as zeros.
+bool make_kv_map_3d(CUtensorMap* m, const void* ptr, uint64_t items, uint64_t rows, uint64_t Lmax) {
+  if (!get_encoder()) return false;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(kHeadDim), static_cast<cuuint64_t>(rows),
+                        static_cast<cuuint64_t>(items)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(kHeadDim) * 2, static_cast<cuuint64_t>(Lmax * kHeadDim * 2)};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(kWfSeg), 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
@@ -287,6 +303,23 @@ BwdLayout bwd_layout(const infllmv2_params* p, int32_t L) {
   return w;
 }
 
+// Row tiles and key splits of the window attention's forward.  A row tile (two 128-row query
+// tiles) is one CTA; when the tiles leave more than half of the SMs idle, the keys of each are
+// split over up to 32 CTAs and joined through the workspace.
+struct WindowPlan {
+  int row_tiles;
+  long long items;  // row_tiles * B * Hkv
+  int n_splits;
+};
+WindowPlan window_plan(const infllmv2_params* p, int32_t Lq) {
+  WindowPlan d;
+  const int tokens = 256 / (p->num_q_heads / p->num_kv_heads);
+  d.row_tiles = (Lq + tokens - 1) / tokens;
+  d.items = static_cast<long long>(d.row_tiles) * p->batch * p->num_kv_heads;
+  d.n_splits = static_cast<int>(std::max<long long>(1, std::min<long long>(32, num_sms() / d.items)));
+  return d;
+}
+
 size_t ws_size(const infllmv2_params* p, int op, int32_t L) {
   if (check_params(p) != INFLLMV2_OK || check_len(L) != INFLLMV2_OK) return static_cast<size_t>(-1);
   switch (op) {
@@ -306,7 +339,10 @@ size_t ws_size(const infllmv2_params* p, int op, int32_t L) {
     }
     case INFLLMV2_OP_QK_NORM_ROPE_BACKWARD:
       return static_cast<size_t>(kNrMaxParts) * 2 * kHeadDim * sizeof(float);
-    case INFLLMV2_OP_WINDOW_ATTN:
+    case INFLLMV2_OP_WINDOW_ATTN: {
+      const WindowPlan d = window_plan(p, L);
+      return d.n_splits == 1 ? 0 : static_cast<size_t>(d.items) * d.n_splits * 256 * (kHeadDim + 1) * sizeof(float);
+    }
     case INFLLMV2_OP_WINDOW_DECODE:
     case INFLLMV2_OP_WINDOW_BACKWARD:
       return 0;
@@ -487,6 +523,34 @@ int select_prefill(const infllmv2_params* p, const void* q, int32_t Lq, const vo
   const size_t smem = sel_prefill_smem_bytes(nblk_cap);
   if ((st = set_smem(reinterpret_cast<const void*>(select_prefill_kernel), smem)) != INFLLMV2_OK) return st;
   select_prefill_kernel<<<static_cast<unsigned>(grid), kSelThreads, smem, s>>>(tm_kc, a);
+  return launch_status();
+}
+
+// Forward of the window attention on the tensor cores.
+int launch_window(const infllmv2_params* p, const WinParams& w, void* ws, cudaStream_t s) {
+  const WindowPlan d = window_plan(p, w.Lq);
+  WinTcParams a;
+  a.w = w;
+  a.g_log2 = 0;
+  while ((1 << a.g_log2) < w.G) ++a.g_log2;
+  a.row_tiles = d.row_tiles;
+  a.n_splits = d.n_splits;
+  a.part_o = static_cast<float*>(ws);
+  a.part_lse = d.n_splits > 1 ? a.part_o + static_cast<size_t>(d.items) * d.n_splits * 256 * kHeadDim : nullptr;
+  const uint64_t items = static_cast<uint64_t>(w.B) * w.Hkv;
+  const uint64_t sinks = static_cast<uint64_t>(std::max(1, std::min(w.n_sink, w.Lmax)));
+  CUtensorMap tq, tk, tv, tks, tvs;
+  if (!make_q_map_3d(&tq, w.q, static_cast<uint64_t>(w.B) * w.Lq, w.Hq, w.G) ||
+      !make_kv_map_3d(&tk, w.k, items, w.Lmax, w.Lmax) || !make_kv_map_3d(&tv, w.v, items, w.Lmax, w.Lmax) ||
+      !make_kv_map_3d(&tks, w.k, items, sinks, w.Lmax) || !make_kv_map_3d(&tvs, w.v, items, sinks, w.Lmax))
+    return INFLLMV2_ERR_CUDA;
+  const size_t smem = window_tc_smem_bytes();
+  int st = set_smem(reinterpret_cast<const void*>(window_tc_kernel), smem);
+  if (st != INFLLMV2_OK) return st;
+  window_tc_kernel<<<static_cast<unsigned>(d.items * d.n_splits), kWfThreads, smem, s>>>(tq, tk, tv, tks, tvs, a);
+  if ((st = launch_status()) != INFLLMV2_OK || d.n_splits == 1) return st;
+  const long long rows = static_cast<long long>(w.B) * w.Lq * w.Hq;
+  window_merge_kernel<<<static_cast<unsigned>((rows + 7) / 8), 256, 0, s>>>(a);
   return launch_status();
 }
 
@@ -1036,9 +1100,7 @@ int infllmv2_window_attn(const infllmv2_params* p, const void* q, int32_t Lq, co
   if (need > 0 && (ws == nullptr || ws_bytes < need || !aligned16(ws))) return INFLLMV2_ERR_WORKSPACE;
   a.o = static_cast<__nv_bfloat16*>(o);
   a.lse = lse;
-  const long long rows = static_cast<long long>(a.B) * a.Lq * a.Hq;
-  window_rows_kernel<<<static_cast<unsigned>((rows + 3) / 4), 128, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a, 0);
-  return launch_status();
+  return launch_window(p, a, ws, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int infllmv2_window_attn_decode(const infllmv2_params* p, const void* q, const void* k_cache, const void* v_cache,

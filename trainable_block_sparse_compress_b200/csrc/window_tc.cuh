@@ -1,0 +1,498 @@
+// window_tc.cuh -- forward of the sliding-window attention (csrc/window.cuh states it) on the
+// 5th-generation tensor cores (tcgen05 + TMEM).
+//
+// A CTA takes two 128-row query tiles of one (sequence, kv-head): row = (token, head of the
+// group), 128 / G tokens x G heads, so the group's heads share every K/V tile and a short
+// window wastes few masked keys (the union of 256 / G tokens' windows).  The keys that any of
+// the CTA's queries sees form at most two runs, the sinks and the window; they are cut into
+// segments of 64 keys that start exactly at the run's first key, and two segments make a
+// 128-key tile, so a few sinks cost half a tile.
+//   warp 8  (one thread, TMA) streams Q once and K / V tiles through one ring of 32 KB slots
+//           (order K0 V0 K1 V1 ..., also the order in which they are released);
+//   warp 9  (one thread) issues S_x = Q_x K^T (M128 N128 K16 x 8) and O_x += P_x V (A = P from
+//           TMEM, V through an MN-major descriptor) for the two query tiles x in turn, so one
+//           tile's products run under the other tile's softmax;
+//   warps 0-3 / 4-7: one softmax warpgroup per query tile, thread = row: no shuffles.  The
+//           reference maximum follows the running maximum lazily: only when a warp holds a row
+//           whose maximum rose by more than 2^8 is O rescaled (in TMEM, after the last product
+//           into it has finished); P <= 2^8 stays exact enough in bf16 and the sums are fp32.
+// P (bf16) overwrites S in TMEM: 64 of its 128 columns, written in two halves so the first
+// four K-steps of P V start before the second half's exponentials.  TMEM: S0 S1 O0 O1, all 512
+// columns.
+#pragma once
+#include "common.cuh"
+#include "tcgen05.cuh"
+#include "window.cuh"
+
+namespace infllmv2 {
+
+constexpr int kWfTileBytes = 128 * 128 * 2;  // 32 KB: 128 rows of Q, K or V (two 64-column halves)
+constexpr int kWfHalf = kWfTileBytes / 2;
+constexpr int kWfSeg = 64;                   // keys of a segment
+constexpr int kWfSlots = 5;
+constexpr int kWfThreads = 32 * 10;
+constexpr int kWfTmaWarp = 8, kWfMmaWarp = 9;
+constexpr uint32_t kWfColO = 256;
+
+struct WfSmem {
+  uint64_t q_full[2], full[kWfSlots], empty[kWfSlots], s_full[2], p_full[2][2], o_full[2], mma_done, tail;
+  uint32_t tmem_base;
+  volatile int abort;
+};
+
+constexpr size_t window_tc_smem_bytes() {
+  return 1024 + static_cast<size_t>(2 + kWfSlots) * kWfTileBytes + sizeof(WfSmem);
+}
+static_assert(window_tc_smem_bytes() <= 227 * 1024, "shared memory of one CTA");
+
+// D[tmem] (+)= A[tmem] * B[smem]: A holds bf16 pairs, 8 columns for 16 values of K.
+__device__ __forceinline__ void umma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %6, %7, %8}, p;\n\t}"
+      ::"r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(0u), "r"(0u), "r"(0u), "r"(0u)
+      : "memory");
+}
+
+// 32 columns of this thread's TMEM lane into v[0..31], without the wait (tmem_wait_ld follows).
+__device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t* v) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+        "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+        "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Waits for every load of this thread and ties the registers to the wait, so no use of them is
+// scheduled before it.
+template <int N>
+__device__ __forceinline__ void tmem_wait_ld_tied(uint32_t (&v)[N]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(v[i]));
+}
+
+__device__ __forceinline__ void tmem_st32_nowait(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+      ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+      "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]),
+      "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]),
+      "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Bits 0 .. n-1 of a 64-bit mask (none for n <= 0, all for n >= 64).
+__device__ __forceinline__ uint64_t low_bits(long long n) {
+  return n <= 0 ? 0ull : (n >= 64 ? ~0ull : (1ull << n) - 1ull);
+}
+
+// The keys of a CTA's queries, as segments of 64: `ns` segments of sinks from key 0, then `nw`
+// segments from key `lo`.  When the sinks reach the window there is one run, from key 0.
+struct WinRuns {
+  int ns, nw, lo, n_sink, t_max;
+  __device__ WinRuns(int t_min, int t_max_, int window, int n_sink_) : n_sink(n_sink_), t_max(t_max_) {
+    const int a = max(0, t_min - window + 1);
+    const bool one = n_sink_ >= a;
+    lo = one ? 0 : a;
+    ns = one ? 0 : (n_sink_ + kWfSeg - 1) / kWfSeg;
+    nw = (t_max_ - lo + kWfSeg) / kWfSeg;
+  }
+  __device__ int tiles() const { return (ns + nw + 1) / 2; }
+  __device__ bool is_sink(int seg) const { return seg < ns; }
+  __device__ int first_key(int seg) const { return seg < ns ? seg * kWfSeg : lo + (seg - ns) * kWfSeg; }
+  // keys of segment `seg` that the query at t sees
+  __device__ uint64_t mask(int seg, int t, int window) const {
+    const int u0 = first_key(seg);
+    const uint64_t past = low_bits(static_cast<long long>(t) - u0 + 1);
+    const uint64_t sink = low_bits(static_cast<long long>(n_sink) - u0);
+    if (is_sink(seg)) return past & sink;
+    return past & (sink | ~low_bits(static_cast<long long>(t) - window - u0 + 1));
+  }
+};
+
+struct WinTcParams {
+  WinParams w;
+  int g_log2;          // log2 of the group size
+  int row_tiles;       // 256-row tiles per (sequence, kv-head)
+  int n_splits;        // key splits of a row tile (1: O and lse are written directly)
+  float* part_o;       // splits: [CTA][256][128] normalised partial outputs
+  float* part_lse;     // [CTA][256] base-2 log-sum-exps (-inf: no key)
+};
+
+// grid = row_tiles * B * Hkv * n_splits (the last row tiles, which see the most keys, first).
+__global__ void __launch_bounds__(kWfThreads, 1)
+    window_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_ks,
+                     const __grid_constant__ CUtensorMap tm_vs, const WinTcParams p) {
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* base = align_smem(smem_raw, 1024);
+  unsigned char* qs = base;                        // two query tiles
+  unsigned char* ring = base + 2 * kWfTileBytes;   // K / V slots
+  WfSmem& S = *reinterpret_cast<WfSmem*>(ring + kWfSlots * kWfTileBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const WinParams& w = p.w;
+
+  int bid = blockIdx.x;
+  const int split = bid % p.n_splits;
+  bid /= p.n_splits;
+  const int bg = bid % (w.B * w.Hkv);
+  const int tile = p.row_tiles - 1 - bid / (w.B * w.Hkv);
+  const int b = bg / w.Hkv, g = bg - b * w.Hkv;
+  const int tt = 128 >> p.g_log2;  // tokens of a 128-row tile
+  const int r0 = tile * 2 * tt;
+  const ChunkLens c = chunk_lens(w.q_lens, w.kv_lens, b, w.Lq, w.Lmax);
+  if (r0 >= c.q_len) return;
+  const int pos0 = c.kv_len - c.q_len;
+  const WinRuns runs(pos0 + r0, pos0 + min(r0 + 2 * tt, c.q_len) - 1, w.window, w.n_sink);
+  // key tiles of this split, and of each query tile within them
+  const int all = runs.tiles(), per = (all + p.n_splits - 1) / p.n_splits;
+  const int j0 = min(split * per, all), j1 = min(j0 + per, all);
+  int jb[2], je[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int ra = r0 + x * tt, rb = min(ra + tt, c.q_len) - 1;  // first and last row
+    const int skip = runs.ns == 0 && w.n_sink == 0 ? max(0, pos0 + ra - w.window + 1 - runs.lo) / 128 : 0;
+    const int end = (runs.ns + (pos0 + rb - runs.lo) / kWfSeg) / 2 + 1;
+    jb[x] = max(j0, skip);
+    je[x] = ra < c.q_len ? min(j1, end) : 0;
+    if (je[x] <= jb[x]) jb[x] = je[x] = 0;
+  }
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kWfSlots; ++s) {
+      mbar_init(&S.full[s], 1);
+      mbar_init(&S.empty[s], 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&S.q_full[x], 1);
+      mbar_init(&S.s_full[x], 1);
+      mbar_init(&S.p_full[x][0], 4);
+      mbar_init(&S.p_full[x][1], 4);
+      mbar_init(&S.o_full[x], 1);
+    }
+    mbar_init(&S.mma_done, 1);
+    mbar_init(&S.tail, 1);
+    S.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kWfMmaWarp) {
+    tmem_alloc(&S.tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = S.tmem_base;
+
+  if (warp == kWfTmaWarp) {
+    // ------------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      for (int x = 0; x < 2; ++x)
+        if (je[x] > jb[x]) {
+          mbar_arrive_expect_tx(&S.q_full[x], kWfTileBytes);
+          for (int h = 0; h < 2; ++h)
+            tma_load_3d(qs + x * kWfTileBytes + h * kWfHalf, &tm_q, &S.q_full[x], 64 * h, g << p.g_log2,
+                        b * w.Lq + r0 + x * tt);
+        }
+    }
+    int slot = 0;
+    uint32_t round = 0, issued = 0;
+    bool tail_used = false, stop = false;
+    for (int j = j0; j < j1 && !stop; ++j)
+      for (int kv = 0; kv < 2; ++kv) {
+        if (round > 0) mbar_wait(&S.empty[slot], (round - 1u) & 1u, &S.abort);
+        stop = __any_sync(0xffffffffu, S.abort != 0);
+        if (stop) break;
+        unsigned char* dst = ring + slot * kWfTileBytes;
+        // rows of V past the cache's end may hold anything (0 x NaN is not 0): such a tile lands on
+        // a barrier of its own and is cleaned before it is handed on
+        int clean[2];
+        bool any = false;
+        for (int s = 0; s < 2; ++s) {
+          const int seg = 2 * j + s;
+          clean[s] = seg < runs.ns + runs.nw && !runs.is_sink(seg) ? c.kv_len - runs.first_key(seg) : kWfSeg;
+          any |= kv == 1 && w.kv_lens != nullptr && clean[s] < kWfSeg;
+        }
+        if (lane == 0) {
+          uint64_t* bar = any ? &S.tail : &S.full[slot];
+          mbar_arrive_expect_tx(bar, kWfTileBytes);
+          for (int s = 0; s < 2; ++s) {
+            const int seg = 2 * j + s;
+            const bool pad = seg >= runs.ns + runs.nw;  // an odd count: rows past the tensor, zero-filled
+            const CUtensorMap* m = runs.is_sink(seg) ? (kv ? &tm_vs : &tm_ks) : (kv ? &tm_v : &tm_k);
+            const int key = pad ? w.Lmax : runs.first_key(seg);
+            for (int h = 0; h < 2; ++h)
+              tma_load_3d(dst + h * kWfHalf + s * (kWfSeg * 128), m, bar, 64 * h, key, bg);
+          }
+        }
+        ++issued;
+        if (any) {
+          tail_used = true;
+          if (mbar_wait(&S.tail, 0, &S.abort))
+            for (int s = 0; s < 2; ++s)
+              for (int i = max(clean[s], 0) * 8 + lane; i < kWfSeg * 8; i += 32)
+                for (int h = 0; h < 2; ++h)
+                  *reinterpret_cast<uint4*>(dst + h * kWfHalf + s * (kWfSeg * 128) + i * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&S.full[slot]);
+        }
+        __syncwarp();
+        if (++slot == kWfSlots) {
+          slot = 0;
+          ++round;
+        }
+      }
+    if (S.abort && lane == 0) {  // let every copy this thread issued land before the CTA ends
+      for (int x = 0; x < 2; ++x)
+        if (je[x] > jb[x]) mbar_wait_drain(&S.q_full[x], 0);
+      for (uint32_t s = 0; s < kWfSlots; ++s)
+        if (issued > s) mbar_wait_drain(&S.full[s], ((issued - 1u - s) / kWfSlots) & 1u);
+      if (tail_used) mbar_wait_drain(&S.tail, 0);
+    }
+    return;
+  }
+
+  if (warp == kWfMmaWarp) {
+    // -------------------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t id_qk = idesc_bf16_f32(128, 128, false, false), id_pv = idesc_bf16_f32(128, 128, false, true);
+      const uint32_t q0 = smem_u32(qs), r0a = smem_u32(ring);
+      uint32_t np[2] = {0, 0};  // probability tiles consumed per query tile
+      auto issue_qk = [&](int x, int slot) {
+        const uint32_t qa = q0 + x * kWfTileBytes, ka = r0a + slot * kWfTileBytes;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t o = static_cast<uint32_t>((k >> 2) * kWfHalf + (k & 3) * 32);
+          umma_bf16(tmem + 128u * x, desc_k_sw128(qa + o), desc_k_sw128(ka + o), id_qk, k > 0 ? 1u : 0u);
+        }
+        umma_commit(&S.s_full[x]);
+      };
+      // item n of the ring: K of tile j is n = 2 (j - j0), V is n + 1
+      auto slot_of = [](int n) { return n % kWfSlots; };
+      auto wait_item = [&](int n) {
+        const bool ok = mbar_wait(&S.full[slot_of(n)], static_cast<uint32_t>(n / kWfSlots) & 1u, &S.abort);
+        tc_fence_after();
+        return ok;
+      };
+      for (int x = 0; x < 2; ++x)
+        if (je[x] > jb[x]) mbar_wait(&S.q_full[x], 0, &S.abort);
+      for (int j = j0 - 1; j < j1; ++j) {
+        const int nv = 2 * (j - j0) + 1, nk = nv + 1;
+        if (j >= j0 && !wait_item(nv)) break;
+        if (j + 1 < j1 && !wait_item(nk)) break;
+        bool ok = true;
+        for (int x = 0; x < 2; ++x) {
+          if (j >= jb[x] && j < je[x]) {
+            const uint32_t va = r0a + slot_of(nv) * kWfTileBytes;
+            for (int h = 0; h < 2 && ok; ++h) {
+              ok = mbar_wait(&S.p_full[x][h], np[x] & 1u, &S.abort);
+              tc_fence_after();
+#pragma unroll
+              for (int k = 4 * h; k < 4 * h + 4; ++k)
+                umma_bf16_ta(tmem + kWfColO + 128u * x, tmem + 128u * x + 8u * k,
+                             desc_mn_sw128(va + k * 2048, kWfHalf, 1024), id_pv, (np[x] > 0 || k > 0) ? 1u : 0u);
+            }
+            if (!ok) break;
+            umma_commit(&S.o_full[x]);
+            ++np[x];
+          }
+          if (x == 1 && j >= j0) umma_commit(&S.empty[slot_of(nv)]);
+          if (j + 1 >= jb[x] && j + 1 < je[x]) issue_qk(x, slot_of(nk));
+        }
+        if (!ok) break;
+        if (j + 1 < j1) umma_commit(&S.empty[slot_of(nk)]);
+      }
+      umma_commit(&S.mma_done);
+    }
+    __syncwarp();
+    named_bar_sync(1, 32 * 9);  // the softmax warps have used TMEM for the last time
+    if (lane == 0) mbar_wait_drain(&S.mma_done, 0);
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+    return;
+  }
+
+  // ------------------------------------------------------------------- softmax warpgroups
+  const int x = warp >> 2;
+  const int row = threadIdx.x & 127;
+  const int r = r0 + x * tt + (row >> p.g_log2);
+  const bool valid = r < c.q_len;
+  const bool warp_live = __any_sync(0xffffffffu, valid);
+  const int t = pos0 + min(r, c.q_len - 1);
+  const int tx_min = pos0 + r0 + x * tt, tx_max = pos0 + min(r0 + (x + 1) * tt, c.q_len) - 1;
+  const uint32_t tl = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+  const uint32_t ts = tl + 128u * x, to = tl + kWfColO + 128u * x;
+  const float sl2 = w.scale_log2;
+  float m2 = -INFINITY, sum = 0.f;  // reference maximum (scaled, base 2) and sum of the row
+  uint32_t n = 0;
+  for (int j = jb[x]; j < je[x]; ++j, ++n) {
+    mbar_wait(&S.s_full[x], n & 1u, &S.abort);  // after a timeout the loop runs on: its loads are collective
+    tc_fence_after();
+    if (warp_live) {
+      uint32_t v[128];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tmem_ld32_nowait(ts + 32 * q, v + 32 * q);
+      tmem_wait_ld_tied(v);
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int seg = 2 * j + s, u0 = runs.first_key(seg);
+        const bool full = u0 + kWfSeg - 1 <= tx_min &&
+                          (runs.is_sink(seg) ? u0 + kWfSeg <= w.n_sink
+                                             : (u0 > tx_max - w.window || u0 + kWfSeg <= w.n_sink));
+        if (!full) {
+          const uint64_t mk = runs.mask(seg, t, w.window);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t bits = static_cast<uint32_t>(mk >> (32 * h));
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!((bits >> i) & 1u)) v[64 * s + 32 * h + i] = 0xff800000u;  // -inf
+          }
+        }
+      }
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int i = 0; i < 128; i += 4)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], __uint_as_float(v[i + q]));
+      const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
+      // the row's reference moves when its maximum is 2^8 above it (from -inf: always)
+      if (__any_sync(0xffffffffu, mt > m2 + 8.f)) {
+        const float mn = fmaxf(m2, mt);
+        const float f = mn == -INFINITY ? 1.f : ex2(m2 - mn);
+        m2 = mn;
+        sum *= f;
+        if (n > 0) {
+          mbar_wait(&S.o_full[x], (n - 1u) & 1u, &S.abort);
+          tc_fence_after();
+#pragma unroll 1
+          for (int q = 0; q < 8; ++q) {
+            uint32_t o16[16];
+            tmem_ld16(to + 16 * q, o16);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o16[i] = __float_as_uint(__uint_as_float(o16[i]) * f);
+            tmem_st16(to + 16 * q, o16);
+          }
+        }
+      }
+      const float mr = m2 == -INFINITY ? 0.f : m2;  // nothing visible yet: every exponential is 0
+      float sm[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int i = 0; i < 64; i += 4) {
+          float e[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            e[q] = ex2(fmaf(__uint_as_float(v[64 * h + i + q]), sl2, -mr));
+            sm[q] += e[q];
+          }
+          pk[i / 2] = pack_bf16(e[0], e[1]);
+          pk[i / 2 + 1] = pack_bf16(e[2], e[3]);
+        }
+        tmem_st32_nowait(ts + 32 * h, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.p_full[x][h]);
+      }
+      sum += (sm[0] + sm[1]) + (sm[2] + sm[3]);
+    } else {  // no row of this warp exists: its lanes of P and O are never read
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&S.p_full[x][0]);
+        mbar_arrive(&S.p_full[x][1]);
+      }
+    }
+  }
+  if (n > 0) mbar_wait(&S.o_full[x], (n - 1u) & 1u, &S.abort);
+  tc_fence_after();
+  if (warp_live) {
+    const int h = (g << p.g_log2) + (row & ((1 << p.g_log2) - 1));
+    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    const float lse2 = sum > 0.f ? m2 + lg2(sum) : -INFINITY;
+    const size_t orow = (static_cast<size_t>(b) * w.Lq + r) * w.Hq + h;
+    const size_t prow = (static_cast<size_t>(blockIdx.x) * 2 + x) * 128 + row;
+    if (valid) {
+      if (p.n_splits > 1)
+        p.part_lse[prow] = lse2;
+      else if (w.lse)
+        w.lse[(static_cast<size_t>(b) * w.Hq + h) * w.Lq + r] = lse2 * 0.6931471805599453f;
+    }
+    if (n > 0)
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        uint32_t v[32];
+        tmem_ld32(to + 32 * q, v);
+        if (valid && p.n_splits > 1) {
+          float4* dst = reinterpret_cast<float4*>(p.part_o + prow * kHeadDim + 32 * q);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            dst[i] = make_float4(__uint_as_float(v[4 * i]) * inv, __uint_as_float(v[4 * i + 1]) * inv,
+                                 __uint_as_float(v[4 * i + 2]) * inv, __uint_as_float(v[4 * i + 3]) * inv);
+        } else if (valid) {
+          uint4* dst = reinterpret_cast<uint4*>(w.o + orow * kHeadDim + 32 * q);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t u[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              u[e] = pack_bf16(__uint_as_float(v[8 * i + 2 * e]) * inv, __uint_as_float(v[8 * i + 2 * e + 1]) * inv);
+            dst[i] = make_uint4(u[0], u[1], u[2], u[3]);
+          }
+        }
+        __syncwarp();
+      }
+  }
+  tc_fence_before();
+  named_bar_sync(1, 32 * 9);  // TMEM may be freed
+}
+
+// Joins the key splits of a row: one warp per (sequence, query row, q-head).  The weights are
+// 2^(lse_s - lse); splits without a visible key (lse -inf) are not read.
+__global__ void __launch_bounds__(256) window_merge_kernel(const WinTcParams p) {
+  const WinParams& w = p.w;
+  const int lane = threadIdx.x & 31;
+  const long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (row >= static_cast<long long>(w.B) * w.Lq * w.Hq) return;
+  const int h = static_cast<int>(row % w.Hq), r = static_cast<int>(row / w.Hq % w.Lq);
+  const int b = static_cast<int>(row / w.Hq / w.Lq);
+  const ChunkLens c = chunk_lens(w.q_lens, w.kv_lens, b, w.Lq, w.Lmax);
+  if (r >= c.q_len) return;
+  const int tt = 128 >> p.g_log2, tile = r / (2 * tt);
+  const int bg = b * w.Hkv + (h >> p.g_log2);
+  const size_t cta = (static_cast<size_t>(p.row_tiles - 1 - tile) * w.B * w.Hkv + bg) * p.n_splits;
+  const size_t in = static_cast<size_t>(r - tile * 2 * tt) * w.G + (h & (w.G - 1));  // row of the CTA's 256
+  float mx = -INFINITY;
+  for (int s = 0; s < p.n_splits; ++s) mx = fmaxf(mx, p.part_lse[(cta + s) * 256 + in]);
+  float acc[4] = {0.f, 0.f, 0.f, 0.f}, z = 0.f;
+  for (int s = 0; s < p.n_splits; ++s) {
+    const float l = p.part_lse[(cta + s) * 256 + in];
+    if (l == -INFINITY) continue;
+    const float e = ex2(l - mx);
+    const float4 o = *(reinterpret_cast<const float4*>(p.part_o + ((cta + s) * 256 + in) * kHeadDim) + lane);
+    z += e;
+    acc[0] = fmaf(e, o.x, acc[0]), acc[1] = fmaf(e, o.y, acc[1]);
+    acc[2] = fmaf(e, o.z, acc[2]), acc[3] = fmaf(e, o.w, acc[3]);
+  }
+  const float inv = 1.f / z;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] *= inv;
+  store4(w.o + row * kHeadDim, lane, acc);
+  if (w.lse && lane == 0) w.lse[(static_cast<size_t>(b) * w.Hq + h) * w.Lq + r] = (mx + lg2(z)) * 0.6931471805599453f;
+}
+
+}  // namespace infllmv2
