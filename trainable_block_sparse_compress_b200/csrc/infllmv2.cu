@@ -29,6 +29,7 @@
 #include "select_prefill_tc.cuh"
 #include "topk.cuh"
 #include "window.cuh"
+#include "window_bwd_tc.cuh"
 #include "window_tc.cuh"
 
 using namespace infllmv2;
@@ -127,6 +128,22 @@ bool make_kv_map_3d(CUtensorMap* m, const void* ptr, uint64_t items, uint64_t ro
   cuuint32_t box[3] = {64, static_cast<cuuint32_t>(kWfSeg), 1};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS;
+}
+
+// 4-D view [sequence, token, head, 128] of query rows, box {64 columns, G heads, 128 / G tokens,
+// 1}: the rows of a tile past a sequence's Lq tokens read as zeros.
+bool make_q_map_4d(CUtensorMap* m, const void* q, uint64_t B, uint64_t Lq, uint64_t heads, int G) {
+  if (!get_encoder()) return false;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(kHeadDim), static_cast<cuuint64_t>(heads),
+                        static_cast<cuuint64_t>(Lq), static_cast<cuuint64_t>(B)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(kHeadDim) * 2, static_cast<cuuint64_t>(heads * kHeadDim * 2),
+                           static_cast<cuuint64_t>(Lq * heads * kHeadDim * 2)};
+  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(128 / G), 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q), dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
@@ -320,6 +337,49 @@ WindowPlan window_plan(const infllmv2_params* p, int32_t Lq) {
   return d;
 }
 
+// Backward of the window attention: cuts of the key tiles' query ranges (counted for sequences
+// of L tokens).  A key tile of a long range (one that holds sinks, or any while key tiles are
+// fewer than SMs) is cut into chunks of q_tiles query tiles, at least 16 (their partials cost a
+// write and a read of 128 KB), at most so many that kWbMaxParts partials hold them.
+constexpr int kWbMaxParts = 512;
+constexpr size_t kWbPartBytes = 2 * kWbKeys * kHeadDim * sizeof(float);
+struct WindowBwdPlan {
+  int key_tiles, sink_tiles, q_tiles, chunks_s, chunks_w;
+  long long parts;  // partials of all (sequence, kv-head)s
+  size_t lse2, delta, part, total;
+};
+WindowBwdPlan window_bwd_plan(const infllmv2_params* p, int32_t L, int32_t window, int32_t n_sink) {
+  WindowBwdPlan d;
+  const long long G = p->num_q_heads / p->num_kv_heads, items = static_cast<long long>(p->batch) * p->num_kv_heads;
+  d.key_tiles = (L + kWbKeys - 1) / kWbKeys;
+  d.sink_tiles = static_cast<int>(std::min<long long>(d.key_tiles, (static_cast<long long>(n_sink) + kWbKeys - 1) / kWbKeys));
+  long long visits = 0, longest[2] = {0, 0};
+  for (int i = 0; i < d.key_tiles; ++i) {
+    const bool sink = i < d.sink_tiles;
+    const long long u0 = static_cast<long long>(i) * kWbKeys;
+    const long long end = sink ? L : std::min<long long>(L, u0 + kWbKeys - 1 + window);
+    const long long n = ((end - u0) * G + 127) / 128;
+    visits += n;
+    longest[sink] = std::max(longest[sink], n);
+  }
+  long long q = std::max<long long>(16, visits * items / (2 * num_sms()) + 1);
+  for (;; q += q / 4) {
+    d.chunks_s = static_cast<int>(std::max<long long>(1, (longest[1] + q - 1) / q));
+    d.chunks_w = static_cast<int>(std::max<long long>(1, (longest[0] + q - 1) / q));
+    d.parts = items * ((d.chunks_s > 1 ? static_cast<long long>(d.sink_tiles) * d.chunks_s : 0) +
+                       (d.chunks_w > 1 ? static_cast<long long>(d.key_tiles - d.sink_tiles) * d.chunks_w : 0));
+    if (d.parts <= kWbMaxParts) break;
+  }
+  d.q_tiles = static_cast<int>(std::min<long long>(q, 1 << 30));
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  const size_t stats = up(static_cast<size_t>(p->batch) * p->num_q_heads * d.key_tiles * kWbKeys * sizeof(float));
+  d.lse2 = 0;
+  d.delta = stats;
+  d.part = 2 * stats;
+  d.total = d.part + static_cast<size_t>(d.parts) * kWbPartBytes;
+  return d;
+}
+
 size_t ws_size(const infllmv2_params* p, int op, int32_t L) {
   if (check_params(p) != INFLLMV2_OK || check_len(L) != INFLLMV2_OK) return static_cast<size_t>(-1);
   switch (op) {
@@ -344,8 +404,13 @@ size_t ws_size(const infllmv2_params* p, int op, int32_t L) {
       return d.n_splits == 1 ? 0 : static_cast<size_t>(d.items) * d.n_splits * 256 * (kHeadDim + 1) * sizeof(float);
     }
     case INFLLMV2_OP_WINDOW_DECODE:
-    case INFLLMV2_OP_WINDOW_BACKWARD:
       return 0;
+    case INFLLMV2_OP_WINDOW_BACKWARD: {  // for every window and n_sink
+      const WindowBwdPlan d = window_bwd_plan(p, L, L, 0);
+      const long long most = static_cast<long long>(p->batch) * p->num_kv_heads * d.key_tiles *
+                             ((static_cast<long long>(L) * (p->num_q_heads / p->num_kv_heads) + 2047) / 2048 + 1);
+      return d.part + static_cast<size_t>(std::min<long long>(kWbMaxParts, most)) * kWbPartBytes;
+    }
     default:
       return static_cast<size_t>(-1);
   }
@@ -551,6 +616,53 @@ int launch_window(const infllmv2_params* p, const WinParams& w, void* ws, cudaSt
   if ((st = launch_status()) != INFLLMV2_OK || d.n_splits == 1) return st;
   const long long rows = static_cast<long long>(w.B) * w.Lq * w.Hq;
   window_merge_kernel<<<static_cast<unsigned>((rows + 7) / 8), 256, 0, s>>>(a);
+  return launch_status();
+}
+
+// Backward of the window attention (the workspace has window_bwd_plan's layout).
+int launch_window_backward(const infllmv2_params* p, const WinParams& w, void* ws, cudaStream_t s) {
+  const WindowBwdPlan d = window_bwd_plan(p, w.Lq, w.window, w.n_sink);
+  unsigned char* wb = static_cast<unsigned char*>(ws);
+  WinBwdParams a;
+  a.w = w;
+  a.g_log2 = 0;
+  while ((1 << a.g_log2) < w.G) ++a.g_log2;
+  a.Lp = d.key_tiles * kWbKeys;
+  a.lse2 = reinterpret_cast<float*>(wb + d.lse2);
+  a.delta = reinterpret_cast<float*>(wb + d.delta);
+  a.part = reinterpret_cast<float*>(wb + d.part);
+  a.key_tiles = d.key_tiles;
+  a.sink_tiles = d.sink_tiles;
+  a.chunks_s = d.chunks_s;
+  a.chunks_w = d.chunks_w;
+  a.q_tiles = d.q_tiles;
+  a.row_tiles = (w.Lq * w.G + 127) / 128;
+  const uint64_t items = static_cast<uint64_t>(w.B) * w.Hkv;
+  const uint64_t sinks = static_cast<uint64_t>(std::max(1, std::min(w.n_sink, w.Lmax)));
+  CUtensorMap tq, tdo, tk, tv, tks, tvs;
+  if (!make_q_map_4d(&tq, w.q, w.B, w.Lq, w.Hq, w.G) || !make_q_map_4d(&tdo, w.d_o, w.B, w.Lq, w.Hq, w.G) ||
+      !make_kv_map_3d(&tk, w.k, items, w.Lmax, w.Lmax) || !make_kv_map_3d(&tv, w.v, items, w.Lmax, w.Lmax) ||
+      !make_kv_map_3d(&tks, w.k, items, sinks, w.Lmax) || !make_kv_map_3d(&tvs, w.v, items, sinks, w.Lmax))
+    return INFLLMV2_ERR_CUDA;
+  const size_t smem = window_bwd_smem_bytes();
+  int st;
+  if ((st = set_smem(reinterpret_cast<const void*>(window_dkdv_tc_kernel), smem)) != INFLLMV2_OK) return st;
+  if ((st = set_smem(reinterpret_cast<const void*>(window_dq_tc_kernel), smem)) != INFLLMV2_OK) return st;
+  const long long rows = static_cast<long long>(w.B) * a.Lp * w.Hq;
+  const long long ctas = static_cast<long long>(items) * (static_cast<long long>(d.sink_tiles) * d.chunks_s +
+                                                          static_cast<long long>(d.key_tiles - d.sink_tiles) * d.chunks_w);
+  const long long dq_ctas = static_cast<long long>(items) * a.row_tiles;
+  if (ctas > 0x7fffffffLL || dq_ctas > 0x7fffffffLL || items > 65535) return INFLLMV2_ERR_UNSUPPORTED;
+  window_delta_kernel<<<static_cast<unsigned>(std::min<long long>((rows + 15) / 16, 8LL * num_sms())), 256, 0, s>>>(a);
+  window_dkdv_tc_kernel<<<static_cast<unsigned>(ctas), kWbThreads, smem, s>>>(tq, tdo, tk, tv, a);
+  if ((st = launch_status()) != INFLLMV2_OK) return st;
+  const int first = d.chunks_s > 1 ? 0 : d.sink_tiles;
+  const int split = d.chunks_w > 1 ? d.key_tiles - first : (d.chunks_s > 1 ? d.sink_tiles : 0);
+  if (split > 0) {
+    const dim3 grid(static_cast<unsigned>(split) * (2 * kWbKeys / 8), static_cast<unsigned>(items));
+    window_dkdv_merge_kernel<<<grid, 256, 0, s>>>(a, first, split);
+  }
+  window_dq_tc_kernel<<<static_cast<unsigned>(dq_ctas), kWbThreads, smem, s>>>(tq, tdo, tk, tv, tks, tvs, a);
   return launch_status();
 }
 
@@ -1137,11 +1249,7 @@ int infllmv2_window_attn_backward(const infllmv2_params* p, const void* q, const
   a.dq = static_cast<__nv_bfloat16*>(dq);
   a.dk = static_cast<__nv_bfloat16*>(dk);
   a.dv = static_cast<__nv_bfloat16*>(dv);
-  const long long rows = static_cast<long long>(a.B) * a.Lq * a.Hq, keys = static_cast<long long>(a.B) * a.Lq * a.Hkv;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  window_dq_rows_kernel<<<static_cast<unsigned>((rows + 3) / 4), 128, 0, s>>>(a);
-  window_dkdv_rows_kernel<<<static_cast<unsigned>((keys + 3) / 4), 128, 0, s>>>(a);
-  return launch_status();
+  return launch_window_backward(p, a, ws, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

@@ -74,67 +74,4 @@ __global__ void __launch_bounds__(128) window_rows_kernel(const WinParams p, int
   if (p.lse && lane == 0) p.lse[li] = (m + lg2(z)) * 0.6931471805599453f;
 }
 
-// dq: one warp per (sequence, query row, q-head).
-__global__ void __launch_bounds__(128) window_dq_rows_kernel(const WinParams p) {
-  const int lane = threadIdx.x & 31;
-  const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (row >= static_cast<long long>(p.B) * p.Lq * p.Hq) return;
-  const int h = static_cast<int>(row % p.Hq), t = static_cast<int>(row / p.Hq % p.Lq);
-  const int b = static_cast<int>(row / p.Hq / p.Lq);
-  if (t >= chunk_lens(p.q_lens, p.kv_lens, b, p.Lq, p.Lmax).q_len) return;
-  float q[4], g[4], o[4], acc[4] = {0.f, 0.f, 0.f, 0.f};
-  load4(p.q + row * kHeadDim, lane, q);
-  load4(p.d_o + row * kHeadDim, lane, g);
-  load4(p.o_in + row * kHeadDim, lane, o);
-  const float dd = warp_dot4(g, o);
-  const float lse2 = p.lse[(static_cast<size_t>(b) * p.Hq + h) * p.Lq + t] * 1.4426950408889634f;
-  const size_t base = (static_cast<size_t>(b) * p.Hkv + h / p.G) * p.Lmax * kHeadDim;
-  const int lo = max(0, t - p.window + 1);
-  for (int u = min(p.n_sink, lo) > 0 ? 0 : lo; u <= t; ++u) {
-    if (u == p.n_sink && u < lo) u = lo;
-    float kk[4], vv[4];
-    load4(p.k + base + static_cast<size_t>(u) * kHeadDim, lane, kk);
-    load4(p.v + base + static_cast<size_t>(u) * kHeadDim, lane, vv);
-    const float pr = ex2(fmaf(warp_dot4(q, kk), p.scale_log2, -lse2));
-    const float ds = pr * (warp_dot4(g, vv) - dd) * p.scale;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = fmaf(ds, kk[i], acc[i]);
-  }
-  store4(p.dq + row * kHeadDim, lane, acc);
-}
-
-// dk, dv: one warp per (sequence, kv-head, key), over the group's heads and the queries that
-// see the key.
-__global__ void __launch_bounds__(128) window_dkdv_rows_kernel(const WinParams p) {
-  const int lane = threadIdx.x & 31;
-  const long long row = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (row >= static_cast<long long>(p.B) * p.Hkv * p.Lmax) return;
-  const int u = static_cast<int>(row % p.Lmax), g = static_cast<int>(row / p.Lmax % p.Hkv);
-  const int b = static_cast<int>(row / p.Lmax / p.Hkv);
-  const int n = chunk_lens(p.q_lens, p.kv_lens, b, p.Lq, p.Lmax).kv_len;
-  if (u >= n) return;
-  float kk[4], vv[4], dk[4] = {0.f, 0.f, 0.f, 0.f}, dv[4] = {0.f, 0.f, 0.f, 0.f};
-  load4(p.k + row * kHeadDim, lane, kk);
-  load4(p.v + row * kHeadDim, lane, vv);
-  const int t1 = u < p.n_sink ? n : static_cast<int>(min(static_cast<long long>(n), static_cast<long long>(u) + p.window));
-  for (int t = u; t < t1; ++t)
-    for (int h = g * p.G; h < (g + 1) * p.G; ++h) {
-      const size_t qr = ((static_cast<size_t>(b) * p.Lq + t) * p.Hq + h) * kHeadDim;
-      float q[4], go[4], o[4];
-      load4(p.q + qr, lane, q);
-      load4(p.d_o + qr, lane, go);
-      load4(p.o_in + qr, lane, o);
-      const float lse2 = p.lse[(static_cast<size_t>(b) * p.Hq + h) * p.Lq + t] * 1.4426950408889634f;
-      const float pr = ex2(fmaf(warp_dot4(q, kk), p.scale_log2, -lse2));
-      const float ds = pr * (warp_dot4(go, vv) - warp_dot4(go, o)) * p.scale;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        dv[i] = fmaf(pr, go[i], dv[i]);
-        dk[i] = fmaf(ds, q[i], dk[i]);
-      }
-    }
-  store4(p.dk + row * kHeadDim, lane, dk);
-  store4(p.dv + row * kHeadDim, lane, dv);
-}
-
 }  // namespace infllmv2

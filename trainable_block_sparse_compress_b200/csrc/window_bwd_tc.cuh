@@ -1,0 +1,686 @@
+// window_bwd_tc.cuh -- backward of the sliding-window attention (csrc/window.cuh states it) on
+// the 5th-generation tensor cores.
+//
+// Rows are (token, head of the group) as in the forward: 128 / G tokens x G heads a tile.
+//   window_delta_kernel  D = dO . O and lse in base 2, one value per row, laid out row by row
+//           ([B, Hkv, token, head of the group], tokens padded to 128) so that a tile's 128
+//           values are contiguous; rows past a sequence's end get lse = +inf (P = 0) and D = 0.
+//   window_dkdv_tc_kernel  per 128 keys of a (sequence, kv-head), over the query tiles that see
+//           one of them: S^T = K Q^T and dP^T = V dO^T (keys x rows), P^T = exp2(S^T - lse),
+//           dS^T = P^T (dP^T - D), then dV += P^T dO and dK += dS^T Q with P^T and dS^T as A
+//           operands in TMEM (bf16, written over S^T and dP^T): nothing but the Q / dO tiles
+//           passes through shared memory, and the group's heads are summed in the accumulator.
+//   window_dq_tc_kernel  per 128 rows, over the keys that they see: S = Q K^T, dP = dO V^T,
+//           dQ += dS K with dS as the A operand in TMEM.
+// S and dP are computed in both (7 products instead of 5): that keeps dq out of fp32 atomics
+// (its order of sums is fixed) and of a 4-byte accumulator in HBM.
+// A tile of keys that holds sinks is seen by every later query: its query range (and any
+// other, when there are few tiles of keys) is cut into chunks of q_tiles query tiles whose
+// partial sums meet in the workspace; window_dkdv_merge_kernel adds them in order.
+#pragma once
+#include "common.cuh"
+#include "tcgen05.cuh"
+#include "window_tc.cuh"
+
+namespace infllmv2 {
+
+constexpr int kWbThreads = 32 * 10;
+constexpr int kWbTmaWarp = 8, kWbMmaWarp = 9;
+constexpr int kWbSlots = 5;
+constexpr int kWbKeys = 128;  // keys of a dK / dV tile
+
+struct WbSmem {
+  uint64_t res_full, full[kWbSlots], empty[kWbSlots], s_full[2], dp_full, p_full[2], ds_full[2], done, mma_done, tail[2];
+  uint64_t st_full[2], st_empty[2];
+  alignas(16) float stats[2][2][128];  // dK / dV: lse and D of a query tile's rows
+  uint32_t tmem_base;
+  volatile int abort;
+};
+
+constexpr size_t window_bwd_smem_bytes() {
+  return static_cast<size_t>(2 + kWbSlots) * kWfTileBytes + sizeof(WbSmem);
+}
+static_assert(window_bwd_smem_bytes() <= 227 * 1024, "shared memory of one CTA");
+
+struct WinBwdParams {
+  WinParams w;
+  int g_log2, Lp;       // Lp: tokens padded to a multiple of 128
+  float *lse2, *delta;  // [B, Hkv, Lp, G]
+  // dK / dV: key tiles 0 .. sink_tiles-1 have chunks_s chunks of q_tiles query tiles, the others
+  // chunks_w; a kind with more than one chunk goes through the partials
+  int key_tiles, sink_tiles, chunks_s, chunks_w, q_tiles, row_tiles;
+  float* part;          // [chunk slot][dV, dK][128 keys][128]
+};
+
+// One half-warp per row (token, q-head): grid-stride over B * Lp * Hq rows.
+__global__ void __launch_bounds__(256) window_delta_kernel(const WinBwdParams p) {
+  const WinParams& w = p.w;
+  const int l = threadIdx.x & 15;
+  const long long rows = static_cast<long long>(w.B) * p.Lp * w.Hq;
+  const long long stride = static_cast<long long>(gridDim.x) * 16;
+  for (long long base = static_cast<long long>(blockIdx.x) * 16 + (threadIdx.x >> 5) * 2; base < rows; base += stride) {
+    const long long row = base + ((threadIdx.x >> 4) & 1);
+    const int h = static_cast<int>(row % w.Hq), t = static_cast<int>(row / w.Hq % p.Lp);
+    const int b = static_cast<int>(row / w.Hq / p.Lp);
+    const bool in = row < rows && t < chunk_lens(w.q_lens, w.kv_lens, min(b, w.B - 1), w.Lq, w.Lmax).q_len;
+    float s = 0.f;
+    if (in) {
+      const size_t o = ((static_cast<size_t>(b) * w.Lq + t) * w.Hq + h) * kHeadDim;
+      const uint4 ua = *(reinterpret_cast<const uint4*>(w.o_in + o) + l);
+      const uint4 ub = *(reinterpret_cast<const uint4*>(w.d_o + o) + l);
+      const uint32_t xa[4] = {ua.x, ua.y, ua.z, ua.w}, xb[4] = {ub.x, ub.y, ub.z, ub.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s = fmaf(__uint_as_float(xa[i] << 16), __uint_as_float(xb[i] << 16), s);
+        s = fmaf(__uint_as_float(xa[i] & 0xffff0000u), __uint_as_float(xb[i] & 0xffff0000u), s);
+      }
+    }
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d, 16);
+    if (row < rows && l == 0) {
+      const size_t i = ((static_cast<size_t>(b) * w.Hkv + (h >> p.g_log2)) * p.Lp + t) * w.G + (h & (w.G - 1));
+      p.lse2[i] = in ? w.lse[(static_cast<size_t>(b) * w.Hq + h) * w.Lq + t] * 1.4426950408889634f : INFINITY;
+      p.delta[i] = s;
+    }
+  }
+}
+
+// Zeroes rows r0 .. 127 of a 128-row tile (both halves), by one warp.
+__device__ __forceinline__ void zero_tile_rows(unsigned char* tile, int r0, int lane) {
+  for (int i = max(r0, 0) * 8 + lane; i < 128 * 8; i += 32) {
+    *reinterpret_cast<uint4*>(tile + i * 16) = make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4*>(tile + kWfHalf + i * 16) = make_uint4(0, 0, 0, 0);
+  }
+}
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z,
+                                            int u) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(u)
+      : "memory");
+}
+
+// Query tokens that see a key of tile `i`: from its first key to t_end(i) (exclusive).
+__device__ __forceinline__ int window_t_end(const WinParams& w, int i, int len) {
+  if (i * kWbKeys < w.n_sink) return len;
+  return static_cast<int>(min(static_cast<long long>(len), static_cast<long long>(i) * kWbKeys + kWbKeys - 1 + w.window));
+}
+
+// S or dP products: D[tmem] = A[128 rows] * B[128 rows]^T over the 128 head dimensions.
+__device__ __forceinline__ void umma_rows(uint32_t d, uint32_t a, uint32_t b) {
+  constexpr uint32_t id = idesc_bf16_f32(128, 128, false, false);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint32_t o = static_cast<uint32_t>((k >> 2) * kWfHalf + (k & 3) * 32);
+    umma_bf16(d, desc_k_sw128(a + o), desc_k_sw128(b + o), id, k > 0 ? 1u : 0u);
+  }
+}
+// D[tmem] += A[tmem] * B: A holds 64 values of K in the first 32 columns of each of its two
+// 64-column halves, B's 128 rows are the K axis.
+__device__ __forceinline__ void umma_acc(uint32_t d, uint32_t a, uint32_t b, bool first) {
+  constexpr uint32_t id = idesc_bf16_f32(128, 128, false, true);
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    umma_bf16_ta(d, a + 64u * (k >> 2) + 8u * (k & 3), desc_mn_sw128(b + k * 2048, kWfHalf, 1024), id,
+                 (!first || k > 0) ? 1u : 0u);
+}
+
+// grid = B * Hkv * (sink_tiles * chunks_s + (key_tiles - sink_tiles) * chunks_w).
+// TMEM: S^T 0, dP^T 128, dV 256, dK 384.
+__global__ void __launch_bounds__(kWbThreads, 1)
+    window_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+                          const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                          const WinBwdParams p) {
+  extern __shared__ __align__(1024) unsigned char smem_1k[];
+  unsigned char* base = smem_1k;
+  unsigned char* kv = base;                        // K tile, V tile
+  unsigned char* ring = base + 2 * kWfTileBytes;   // Q / dO slots: Q0 dO0 Q1 dO1 ...
+  WbSmem& S = *reinterpret_cast<WbSmem*>(ring + kWbSlots * kWfTileBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const WinParams& w = p.w;
+
+  const int bg = blockIdx.x % (w.B * w.Hkv), e = blockIdx.x / (w.B * w.Hkv);
+  const bool sink_kind = e < p.sink_tiles * p.chunks_s;
+  const int chunks = sink_kind ? p.chunks_s : p.chunks_w;
+  const int e2 = sink_kind ? e : e - p.sink_tiles * p.chunks_s;
+  const int tile = (sink_kind ? 0 : p.sink_tiles) + e2 / chunks, chunk = e2 % chunks;
+  const int b = bg / w.Hkv, g = bg - b * w.Hkv;
+  const int tt = 128 >> p.g_log2;
+  const int len = chunk_lens(w.q_lens, w.kv_lens, b, w.Lq, w.Lmax).q_len;
+  const int u0 = tile * kWbKeys;
+  if (u0 >= len) return;
+  const int t_end = window_t_end(w, tile, len);
+  const int n_all = (t_end - u0 + tt - 1) / tt;
+  const int i0 = chunk * p.q_tiles, i1 = chunks == 1 ? n_all : min(n_all, i0 + p.q_tiles);
+  if (i0 >= i1) return;
+  const int n = i1 - i0;
+  const int ta = u0 + i0 * tt;  // first token
+
+  if (threadIdx.x == 0) {
+    mbar_init(&S.res_full, 1);
+    for (int s = 0; s < kWbSlots; ++s) {
+      mbar_init(&S.full[s], 1);
+      mbar_init(&S.empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&S.s_full[s], 1);
+      mbar_init(&S.p_full[s], 4);
+      mbar_init(&S.ds_full[s], 4);
+      mbar_init(&S.tail[s], 1);
+      mbar_init(&S.st_full[s], 1);
+      mbar_init(&S.st_empty[s], 8);
+    }
+    mbar_init(&S.dp_full, 1);
+    mbar_init(&S.done, 1);
+    mbar_init(&S.mma_done, 1);
+    S.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kWbMmaWarp) {
+    tmem_alloc(&S.tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = S.tmem_base;
+
+  if (warp == kWbTmaWarp) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&S.res_full, 2 * kWfTileBytes);
+      for (int h = 0; h < 2; ++h)
+        for (int s = 0; s < 2; ++s) {
+          tma_load_3d(kv + h * kWfHalf + s * (kWfSeg * 128), &tm_k, &S.res_full, 64 * h, u0 + 64 * s, bg);
+          tma_load_3d(kv + kWfTileBytes + h * kWfHalf + s * (kWfSeg * 128), &tm_v, &S.res_full, 64 * h, u0 + 64 * s,
+                      bg);
+        }
+    }
+    const size_t stat0 = (static_cast<size_t>(bg) * p.Lp + ta) << p.g_log2;
+    int slot = 0;
+    uint32_t round = 0, issued = 0, stats = 0;
+    bool tail_used = false, stop = false;
+    for (int i = 0; i < n && !stop; ++i) {
+      const int t0 = ta + i * tt;
+      const bool any = w.q_lens != nullptr && t0 + tt > len;  // rows past the end may hold anything
+      for (int kd = 0; kd < 2; ++kd) {
+        if (round > 0) mbar_wait(&S.empty[slot], (round - 1u) & 1u, &S.abort);
+        if (kd == 0 && i >= 2) mbar_wait(&S.st_empty[i & 1], static_cast<uint32_t>((i >> 1) - 1) & 1u, &S.abort);
+        stop = __any_sync(0xffffffffu, S.abort != 0);
+        if (stop) break;
+        unsigned char* dst = ring + slot * kWfTileBytes;
+        if (lane == 0) {
+          uint64_t* bar = any ? &S.tail[kd] : &S.full[slot];
+          mbar_arrive_expect_tx(bar, kWfTileBytes);
+          for (int h = 0; h < 2; ++h)
+            tma_load_4d(dst + h * kWfHalf, kd ? &tm_do : &tm_q, bar, 64 * h, g << p.g_log2, t0, b);
+          if (kd == 0) {
+            mbar_arrive_expect_tx(&S.st_full[i & 1], 1024);
+            for (int s = 0; s < 2; ++s)
+              asm volatile(
+                  "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], 512, [%2];" ::"r"(
+                      smem_u32(S.stats[i & 1][s])),
+                  "l"((s ? p.delta : p.lse2) + stat0 + static_cast<size_t>(i) * 128), "r"(smem_u32(&S.st_full[i & 1]))
+                  : "memory");
+          }
+        }
+        if (kd == 0) ++stats;
+        ++issued;
+        if (any) {
+          tail_used = true;
+          if (mbar_wait(&S.tail[kd], 0, &S.abort)) zero_tile_rows(dst, (len - t0) << p.g_log2, lane);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&S.full[slot]);
+        }
+        __syncwarp();
+        if (++slot == kWbSlots) {
+          slot = 0;
+          ++round;
+        }
+      }
+    }
+    if (S.abort && lane == 0) {  // let every copy this thread issued land before the CTA ends
+      mbar_wait_drain(&S.res_full, 0);
+      for (uint32_t s = 0; s < kWbSlots; ++s)
+        if (issued > s) mbar_wait_drain(&S.full[s], ((issued - 1u - s) / kWbSlots) & 1u);
+      for (uint32_t s = 0; s < 2; ++s)
+        if (stats > s) mbar_wait_drain(&S.st_full[s], ((stats - 1u - s) / 2) & 1u);
+      if (tail_used) mbar_wait_drain(&S.tail[0], 0);
+    }
+    return;
+  }
+
+  if (warp == kWbMmaWarp) {
+    if (lane == 0) {
+      const uint32_t ka = smem_u32(kv), va = ka + kWfTileBytes, ra = smem_u32(ring);
+      auto at = [&](int item) { return ra + static_cast<uint32_t>(item % kWbSlots) * kWfTileBytes; };
+      auto wait_item = [&](int item) {
+        const bool ok = mbar_wait(&S.full[item % kWbSlots], static_cast<uint32_t>(item / kWbSlots) & 1u, &S.abort);
+        tc_fence_after();
+        return ok;
+      };
+      // Order: S(0) dP(0) | dV(i) S(i+1) | dK(i) dP(i+1).  dV(i) and S(i+1) run while dS(i) is
+      // formed, dK(i) and dP(i+1) while the exponentials of tile i+1 are.
+      bool ok = mbar_wait(&S.res_full, 0, &S.abort) && wait_item(0);
+      if (ok) {
+        umma_rows(tmem, ka, at(0));
+        umma_commit(&S.s_full[0]);
+        ok = wait_item(1);
+      }
+      if (ok) {
+        umma_rows(tmem + 128, va, at(1));
+        umma_commit(&S.dp_full);
+      }
+      for (int i = 0; i < n && ok; ++i) {
+        for (int h = 0; h < 2 && ok; ++h) ok = mbar_wait(&S.p_full[h], i & 1u, &S.abort);
+        if (!ok) break;
+        tc_fence_after();
+        umma_acc(tmem + 256, tmem, at(2 * i + 1), i == 0);
+        umma_commit(&S.empty[(2 * i + 1) % kWbSlots]);
+        if (i + 1 < n) {
+          if (!wait_item(2 * i + 2)) break;
+          umma_rows(tmem, ka, at(2 * i + 2));
+          umma_commit(&S.s_full[0]);
+        }
+        for (int h = 0; h < 2 && ok; ++h) ok = mbar_wait(&S.ds_full[h], i & 1u, &S.abort);
+        if (!ok) break;
+        tc_fence_after();
+        umma_acc(tmem + 384, tmem + 128, at(2 * i), i == 0);
+        umma_commit(&S.empty[(2 * i) % kWbSlots]);
+        if (i + 1 < n) {
+          if (!wait_item(2 * i + 3)) break;
+          umma_rows(tmem + 128, va, at(2 * i + 3));
+          umma_commit(&S.dp_full);
+        }
+      }
+      umma_commit(&S.done);
+      umma_commit(&S.mma_done);
+    }
+    __syncwarp();
+    named_bar_sync(1, 32 * 9);
+    if (lane == 0) mbar_wait_drain(&S.mma_done, 0);
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+    return;
+  }
+
+  // ---------------------------------------- elementwise: thread = key, a warpgroup half the rows
+  const int wg = warp >> 2;
+  const int key = threadIdx.x & 127, u = u0 + key;
+  const uint32_t tl = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + 64u * wg;
+  const float sl2 = w.scale_log2;
+  // rows (of this warpgroup's 64) whose queries see the key: tokens u .. hi - 1
+  const int hi = u < w.n_sink ? len : static_cast<int>(min(static_cast<long long>(len), static_cast<long long>(u) + w.window));
+  for (int i = 0; i < n; ++i) {
+    const int t0 = ta + i * tt;
+    const bool all = t0 >= u0 + kWbKeys - 1 && t0 + tt <= len &&
+                     (static_cast<long long>(t0) + tt <= static_cast<long long>(u0) + w.window || u0 + kWbKeys <= w.n_sink);
+    uint64_t mk = ~0ull;
+    if (!all)
+      mk = low_bits(static_cast<long long>(hi - t0) * w.G - 64 * wg) &
+           ~low_bits(static_cast<long long>(u - t0) * w.G - 64 * wg);
+    const float4* st = reinterpret_cast<const float4*>(S.stats[i & 1][0] + 64 * wg);
+    const float4* sd = reinterpret_cast<const float4*>(S.stats[i & 1][1] + 64 * wg);
+    mbar_wait(&S.st_full[i & 1], static_cast<uint32_t>(i >> 1) & 1u, &S.abort);
+    mbar_wait(&S.s_full[0], i & 1u, &S.abort);
+    tc_fence_after();
+    uint32_t v[64];  // S^T, then P^T
+    tmem_ld32_nowait(tl, v);
+    tmem_ld32_nowait(tl + 32, v + 32);
+    tmem_wait_ld_tied(v);
+    {
+      uint32_t pk[32];
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        const float4 ls = st[q];
+        const float lv[4] = {ls.x, ls.y, ls.z, ls.w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          float pr = ex2(fmaf(__uint_as_float(v[4 * q + c]), sl2, -lv[c]));
+          if (!all && !((mk >> (4 * q + c)) & 1ull)) pr = 0.f;
+          v[4 * q + c] = __float_as_uint(pr);
+        }
+        pk[2 * q] = pack_bf16(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]));
+        pk[2 * q + 1] = pack_bf16(__uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3]));
+      }
+      tmem_st32_nowait(tl, pk);
+    }
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&S.p_full[wg]);
+    mbar_wait(&S.dp_full, i & 1u, &S.abort);
+    tc_fence_after();
+    uint32_t pk[32];
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      uint32_t d[32];
+      tmem_ld32_nowait(tl + 128 + 32 * hf, d);
+      tmem_wait_ld_tied(d);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const float4 dl = sd[8 * hf + q];
+        const float lv[4] = {dl.x, dl.y, dl.z, dl.w};
+        float ds[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          ds[c] = __uint_as_float(v[32 * hf + 4 * q + c]) * (__uint_as_float(d[4 * q + c]) - lv[c]);
+          if (!all && !((mk >> (32 * hf + 4 * q + c)) & 1ull)) ds[c] = 0.f;
+        }
+        pk[16 * hf + 2 * q] = pack_bf16(ds[0], ds[1]);
+        pk[16 * hf + 2 * q + 1] = pack_bf16(ds[2], ds[3]);
+      }
+    }
+    tmem_st32_nowait(tl + 128, pk);
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive(&S.ds_full[wg]);
+      mbar_arrive(&S.st_empty[i & 1]);
+    }
+  }
+  mbar_wait(&S.done, 0, &S.abort);
+  tc_fence_after();
+  // warpgroup 0 writes dV, warpgroup 1 dK: thread = key, its 128 values contiguous
+  const uint32_t acc = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + 256u + 128u * wg;
+  const float f = wg ? w.scale : 1.f;
+  // slot of the partials: the CTA's place among those of split kinds
+  const int slot = (sink_kind ? 0 : (p.chunks_s > 1 ? p.sink_tiles * p.chunks_s : 0)) + e2;
+  const size_t item = static_cast<size_t>(slot) * (w.B * w.Hkv) + bg;
+#pragma unroll 1
+  for (int q = 0; q < 4; ++q) {
+    uint32_t v[32];
+    __syncwarp();
+    tmem_ld32(acc + 32 * q, v);
+    if (chunks > 1) {
+      float4* dst = reinterpret_cast<float4*>(p.part + ((item * 2 + wg) * kWbKeys + key) * kHeadDim + 32 * q);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        dst[i] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]),
+                             __uint_as_float(v[4 * i + 3]));
+    } else if (u < len) {
+      uint4* dst = reinterpret_cast<uint4*>((wg ? w.dk : w.dv) + (static_cast<size_t>(bg) * w.Lmax + u) * kHeadDim + 32 * q);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t x[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          x[c] = pack_bf16(__uint_as_float(v[8 * i + 2 * c]) * f, __uint_as_float(v[8 * i + 2 * c + 1]) * f);
+        dst[i] = make_uint4(x[0], x[1], x[2], x[3]);
+      }
+    }
+  }
+  tc_fence_before();
+  named_bar_sync(1, 32 * 9);  // TMEM may be freed
+}
+
+// Adds the chunks of the split key tiles in order: a warp per (key, dV or dK) row.
+// grid.x covers the split tiles of one (sequence, kv-head) x 128 keys x 2 / 8, grid.y = B * Hkv.
+__global__ void __launch_bounds__(256) window_dkdv_merge_kernel(const WinBwdParams p, int first_tile, int tiles) {
+  const WinParams& w = p.w;
+  const int lane = threadIdx.x & 31;
+  const int row = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int ti = row / (2 * kWbKeys), which = row / kWbKeys & 1, key = row & (kWbKeys - 1);
+  if (ti >= tiles) return;
+  const int tile = first_tile + ti, bg = blockIdx.y, b = bg / w.Hkv;
+  const int len = chunk_lens(w.q_lens, w.kv_lens, b, w.Lq, w.Lmax).q_len;
+  const int u = tile * kWbKeys + key;
+  if (u >= len) return;
+  const bool sink = tile < p.sink_tiles;
+  const int chunks = sink ? p.chunks_s : p.chunks_w;
+  const int slot0 = sink ? tile * chunks : (p.chunks_s > 1 ? p.sink_tiles * p.chunks_s : 0) + (tile - p.sink_tiles) * chunks;
+  const int tt = 128 >> p.g_log2;
+  const int n_all = (window_t_end(w, tile, len) - tile * kWbKeys + tt - 1) / tt;
+  const int live = min(chunks, (n_all + p.q_tiles - 1) / p.q_tiles);
+  float a[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int c = 0; c < live; ++c) {
+    const size_t item = static_cast<size_t>(slot0 + c) * (w.B * w.Hkv) + bg;
+    const float4 x = *(reinterpret_cast<const float4*>(p.part + ((item * 2 + which) * kWbKeys + key) * kHeadDim) + lane);
+    a[0] += x.x, a[1] += x.y, a[2] += x.z, a[3] += x.w;
+  }
+  if (which)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] *= w.scale;
+  store4((which ? w.dk : w.dv) + (static_cast<size_t>(bg) * w.Lmax + u) * kHeadDim, lane, a);
+}
+
+// grid = row_tiles * B * Hkv, the last row tiles first.  TMEM: S 0 and 128, dP 256, dQ 384.
+__global__ void __launch_bounds__(kWbThreads, 1)
+    window_dq_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+                        const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                        const __grid_constant__ CUtensorMap tm_ks, const __grid_constant__ CUtensorMap tm_vs,
+                        const WinBwdParams p) {
+  extern __shared__ __align__(1024) unsigned char smem_1k[];
+  unsigned char* base = smem_1k;
+  unsigned char* qd = base;                        // Q tile, dO tile
+  unsigned char* ring = base + 2 * kWfTileBytes;   // K / V slots: K0 V0 K1 V1 ...
+  WbSmem& S = *reinterpret_cast<WbSmem*>(ring + kWbSlots * kWfTileBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const WinParams& w = p.w;
+
+  const int bg = blockIdx.x % (w.B * w.Hkv);
+  const int tile = p.row_tiles - 1 - blockIdx.x / (w.B * w.Hkv);
+  const int b = bg / w.Hkv, g = bg - b * w.Hkv;
+  const int tt = 128 >> p.g_log2;
+  const int r0 = tile * tt;
+  const int len = chunk_lens(w.q_lens, w.kv_lens, b, w.Lq, w.Lmax).q_len;
+  if (r0 >= len) return;
+  const int t_last = min(r0 + tt, len) - 1;
+  const WinRuns runs(r0, t_last, w.window, w.n_sink);
+  const int n = runs.tiles();
+
+  if (threadIdx.x == 0) {
+    mbar_init(&S.res_full, 1);
+    for (int s = 0; s < kWbSlots; ++s) {
+      mbar_init(&S.full[s], 1);
+      mbar_init(&S.empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&S.s_full[s], 1);
+      mbar_init(&S.ds_full[s], 4);
+      mbar_init(&S.tail[s], 1);
+    }
+    mbar_init(&S.dp_full, 1);
+    mbar_init(&S.done, 1);
+    mbar_init(&S.mma_done, 1);
+    S.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kWbMmaWarp) {
+    tmem_alloc(&S.tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = S.tmem_base;
+
+  if (warp == kWbTmaWarp) {
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&S.res_full, 2 * kWfTileBytes);
+      for (int h = 0; h < 2; ++h) {
+        tma_load_4d(qd + h * kWfHalf, &tm_q, &S.res_full, 64 * h, g << p.g_log2, r0, b);
+        tma_load_4d(qd + kWfTileBytes + h * kWfHalf, &tm_do, &S.res_full, 64 * h, g << p.g_log2, r0, b);
+      }
+    }
+    int slot = 0;
+    uint32_t round = 0, issued = 0;
+    bool tail_used = false, stop = false;
+    for (int j = 0; j < n && !stop; ++j)
+      for (int kv = 0; kv < 2; ++kv) {
+        if (round > 0) mbar_wait(&S.empty[slot], (round - 1u) & 1u, &S.abort);
+        stop = __any_sync(0xffffffffu, S.abort != 0);
+        if (stop) break;
+        unsigned char* dst = ring + slot * kWfTileBytes;
+        // rows of K past the sequence's end may hold anything (dS there is 0, but 0 x NaN is not)
+        int clean[2];
+        bool any = false;
+        for (int s = 0; s < 2; ++s) {
+          const int seg = 2 * j + s;
+          clean[s] = seg < runs.ns + runs.nw && !runs.is_sink(seg) ? len - runs.first_key(seg) : kWfSeg;
+          any |= kv == 0 && w.kv_lens != nullptr && clean[s] < kWfSeg;
+        }
+        if (lane == 0) {
+          uint64_t* bar = any ? &S.tail[0] : &S.full[slot];
+          mbar_arrive_expect_tx(bar, kWfTileBytes);
+          for (int s = 0; s < 2; ++s) {
+            const int seg = 2 * j + s;
+            const bool pad = seg >= runs.ns + runs.nw;
+            const CUtensorMap* m = runs.is_sink(seg) ? (kv ? &tm_vs : &tm_ks) : (kv ? &tm_v : &tm_k);
+            const int k0 = pad ? w.Lmax : runs.first_key(seg);
+            for (int h = 0; h < 2; ++h)
+              tma_load_3d(dst + h * kWfHalf + s * (kWfSeg * 128), m, bar, 64 * h, k0, bg);
+          }
+        }
+        ++issued;
+        if (any) {
+          tail_used = true;
+          if (mbar_wait(&S.tail[0], 0, &S.abort))
+            for (int s = 0; s < 2; ++s)
+              for (int i = max(clean[s], 0) * 8 + lane; i < kWfSeg * 8; i += 32)
+                for (int h = 0; h < 2; ++h)
+                  *reinterpret_cast<uint4*>(dst + h * kWfHalf + s * (kWfSeg * 128) + i * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&S.full[slot]);
+        }
+        __syncwarp();
+        if (++slot == kWbSlots) {
+          slot = 0;
+          ++round;
+        }
+      }
+    if (S.abort && lane == 0) {
+      mbar_wait_drain(&S.res_full, 0);
+      for (uint32_t s = 0; s < kWbSlots; ++s)
+        if (issued > s) mbar_wait_drain(&S.full[s], ((issued - 1u - s) / kWbSlots) & 1u);
+      if (tail_used) mbar_wait_drain(&S.tail[0], 0);
+    }
+    return;
+  }
+
+  if (warp == kWbMmaWarp) {
+    if (lane == 0) {
+      const uint32_t qa = smem_u32(qd), da = qa + kWfTileBytes, ra = smem_u32(ring);
+      auto at = [&](int item) { return ra + static_cast<uint32_t>(item % kWbSlots) * kWfTileBytes; };
+      auto wait_item = [&](int item) {
+        const bool ok = mbar_wait(&S.full[item % kWbSlots], static_cast<uint32_t>(item / kWbSlots) & 1u, &S.abort);
+        tc_fence_after();
+        return ok;
+      };
+      // Order: S(0) dP(0) S(1) | dP(j+1) dQ(j) S(j+2): the next tile's scores and dP are there when
+      // its exponentials start.
+      auto issue_s = [&](int j) {
+        if (!wait_item(2 * j)) return false;
+        umma_rows(tmem + 128u * (j & 1), qa, at(2 * j));
+        umma_commit(&S.s_full[j & 1]);
+        return true;
+      };
+      auto issue_dp = [&](int j) {
+        if (!wait_item(2 * j + 1)) return false;
+        umma_rows(tmem + 256, da, at(2 * j + 1));
+        umma_commit(&S.dp_full);
+        umma_commit(&S.empty[(2 * j + 1) % kWbSlots]);
+        return true;
+      };
+      bool ok = mbar_wait(&S.res_full, 0, &S.abort) && issue_s(0) && issue_dp(0) && (n < 2 || issue_s(1));
+      for (int j = 0; j < n && ok; ++j) {
+        for (int h = 0; h < 2 && ok; ++h) ok = mbar_wait(&S.ds_full[h], j & 1u, &S.abort);
+        if (!ok) break;
+        tc_fence_after();
+        if (j + 1 < n && !issue_dp(j + 1)) break;
+        umma_acc(tmem + 384, tmem + 128u * (j & 1), at(2 * j), j == 0);
+        umma_commit(&S.empty[(2 * j) % kWbSlots]);
+        if (j + 2 < n && !issue_s(j + 2)) break;
+      }
+      umma_commit(&S.done);
+      umma_commit(&S.mma_done);
+    }
+    __syncwarp();
+    named_bar_sync(1, 32 * 9);
+    if (lane == 0) mbar_wait_drain(&S.mma_done, 0);
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+    return;
+  }
+
+  // ---------------------- elementwise: thread = row, a warpgroup one 64-key segment of the tile
+  const int wg = warp >> 2;
+  const int row = threadIdx.x & 127;
+  const int t = r0 + (row >> p.g_log2);
+  const bool valid = t < len;
+  const size_t si = ((static_cast<size_t>(bg) * p.Lp + r0) << p.g_log2) + row;
+  const float lse2 = p.lse2[si], dl = p.delta[si];
+  const uint32_t lane0 = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+  const float sl2 = w.scale_log2;
+  for (int j = 0; j < n; ++j) {
+    const int seg = 2 * j + wg, u0 = runs.first_key(seg);
+    const bool all = u0 + kWfSeg - 1 <= r0 && t_last == r0 + tt - 1 &&
+                     (runs.is_sink(seg) ? u0 + kWfSeg <= w.n_sink
+                                        : (u0 > t_last - w.window || u0 + kWfSeg <= w.n_sink));
+    const uint64_t mk = all ? ~0ull : (valid ? runs.mask(seg, t, w.window) : 0ull);
+    const uint32_t ts = tmem + lane0 + 128u * (j & 1) + 64u * wg, td = tmem + lane0 + 256u + 64u * wg;
+    mbar_wait(&S.s_full[j & 1], static_cast<uint32_t>(j >> 1) & 1u, &S.abort);
+    tc_fence_after();
+    uint32_t v[64];
+    tmem_ld32_nowait(ts, v);
+    tmem_ld32_nowait(ts + 32, v + 32);
+    tmem_wait_ld_tied(v);
+#pragma unroll
+    for (int c = 0; c < 64; ++c) v[c] = __float_as_uint(ex2(fmaf(__uint_as_float(v[c]), sl2, -lse2)));
+    mbar_wait(&S.dp_full, j & 1u, &S.abort);
+    tc_fence_after();
+    uint32_t pk[32];
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf) {
+      uint32_t d[32];
+      tmem_ld32_nowait(td + 32 * hf, d);
+      tmem_wait_ld_tied(d);
+#pragma unroll
+      for (int c = 0; c < 32; c += 2) {
+        float ds[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          ds[q] = __uint_as_float(v[32 * hf + c + q]) * (__uint_as_float(d[c + q]) - dl);
+          if (!all && !((mk >> (32 * hf + c + q)) & 1ull)) ds[q] = 0.f;
+        }
+        pk[16 * hf + c / 2] = pack_bf16(ds[0], ds[1]);
+      }
+    }
+    tmem_st32_nowait(ts, pk);
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&S.ds_full[wg]);
+  }
+  mbar_wait(&S.done, 0, &S.abort);
+  tc_fence_after();
+  // a warpgroup writes 64 of the row's 128 values
+  const int h = (g << p.g_log2) + (row & (w.G - 1));
+#pragma unroll 1
+  for (int q = 0; q < 2; ++q) {
+    uint32_t v[32];
+    __syncwarp();
+    tmem_ld32(tmem + lane0 + 384u + 64u * wg + 32 * q, v);
+    if (valid) {
+      uint4* dst = reinterpret_cast<uint4*>(w.dq + ((static_cast<size_t>(b) * w.Lq + t) * w.Hq + h) * kHeadDim + 64 * wg + 32 * q);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t x[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          x[c] = pack_bf16(__uint_as_float(v[8 * i + 2 * c]) * w.scale, __uint_as_float(v[8 * i + 2 * c + 1]) * w.scale);
+        dst[i] = make_uint4(x[0], x[1], x[2], x[3]);
+      }
+    }
+  }
+  tc_fence_before();
+  named_bar_sync(1, 32 * 9);  // TMEM may be freed
+}
+
+}  // namespace infllmv2
