@@ -162,6 +162,8 @@ DECODE = [
     (20000, 4, 1, 100000, 0, [20000]),
     (20000, 4, 2, 1, 0, [20000, 5]),
     (40000, 32, 2, 33333, 1, [40000, 39999, 12]),
+    (128, 4, 2, 65, 60, [128, 127, 126, 125, 124, 64]),  # two runs: a segment more than the cache has blocks
+    (64 * 9, 16, 1, 65, 62, [576, 128]),
     (300, 2, 1, 128, 128, [300, 255, 256, 257, 128, 129]),
     (70000, 16, 1, 70000, 0, [70000]),
     (2000, 16, 2, 500, 100, [2000 - 31 * i for i in range(64)]),

@@ -30,6 +30,7 @@
 #include "topk.cuh"
 #include "window.cuh"
 #include "window_bwd_tc.cuh"
+#include "window_decode.cuh"
 #include "window_tc.cuh"
 
 using namespace infllmv2;
@@ -337,6 +338,21 @@ WindowPlan window_plan(const infllmv2_params* p, int32_t Lq) {
   return d;
 }
 
+// Chunks of the window decode.  While every (sequence, kv-head)'s segments make no more than 8
+// per CTA slot (two CTAs an SM), one wave takes them, at least two a chunk; beyond that about six
+// waves of chunks even out ragged lengths.  Counted for full caches of Lmax tokens.
+struct WindowDecodePlan {
+  int per_chunk, chunks;
+};
+WindowDecodePlan window_decode_plan(const infllmv2_params* p, int32_t Lmax, int32_t window, int32_t n_sink) {
+  const long long items = static_cast<long long>(p->batch) * p->num_kv_heads, slots = 2LL * num_sms();
+  const long long win = (std::min<long long>(window, Lmax) + kWfSeg - 1) / kWfSeg;
+  // two runs of keys may make one segment more than one run of the whole cache
+  const long long segs = std::min<long long>(num_blocks(Lmax) + 1, win + (std::min<long long>(n_sink, Lmax) + kWfSeg - 1) / kWfSeg);
+  const long long each = (items * segs + slots - 1) / slots;
+  const long long per = each <= 8 ? std::max<long long>(2, each) : std::max<long long>(8, (each + 5) / 6);
+  return {static_cast<int>(per), static_cast<int>((segs + per - 1) / per)};
+}
 // Backward of the window attention: cuts of the key tiles' query ranges (counted for sequences
 // of L tokens).  A key tile of a long range (one that holds sinks, or any while key tiles are
 // fewer than SMs) is cut into chunks of q_tiles query tiles, at least 16 (their partials cost a
@@ -403,8 +419,12 @@ size_t ws_size(const infllmv2_params* p, int op, int32_t L) {
       const WindowPlan d = window_plan(p, L);
       return d.n_splits == 1 ? 0 : static_cast<size_t>(d.items) * d.n_splits * 256 * (kHeadDim + 1) * sizeof(float);
     }
-    case INFLLMV2_OP_WINDOW_DECODE:
-      return 0;
+    case INFLLMV2_OP_WINDOW_DECODE: {  // for every window and n_sink: window_decode_plan's chunks at most
+      const size_t items = static_cast<size_t>(p->batch) * p->num_kv_heads, segs = num_blocks(L) + 1;
+      if (segs <= 2) return 0;
+      const size_t most = std::min<size_t>(12 * static_cast<size_t>(num_sms()) + items, items * ((segs + 1) / 2));
+      return most * (p->num_q_heads / p->num_kv_heads) * (kHeadDim + 1) * sizeof(float);
+    }
     case INFLLMV2_OP_WINDOW_BACKWARD: {  // for every window and n_sink
       const WindowBwdPlan d = window_bwd_plan(p, L, L, 0);
       const long long most = static_cast<long long>(p->batch) * p->num_kv_heads * d.key_tiles *
@@ -617,6 +637,49 @@ int launch_window(const infllmv2_params* p, const WinParams& w, void* ws, cudaSt
   const long long rows = static_cast<long long>(w.B) * w.Lq * w.Hq;
   window_merge_kernel<<<static_cast<unsigned>((rows + 7) / 8), 256, 0, s>>>(a);
   return launch_status();
+}
+
+// Launches `kern` so that it may start while the previous kernel on the stream finishes (it
+// calls grid_dependency_wait() before it reads anything that kernel wrote).
+template <typename... Params, typename... Args>
+int launch_pdl(void (*kern)(Params...), unsigned grid, int threads, size_t smem, cudaStream_t s, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...) == cudaSuccess ? INFLLMV2_OK : INFLLMV2_ERR_CUDA;
+}
+
+int launch_window_decode(const infllmv2_params* p, const WinParams& w, void* ws, cudaStream_t s) {
+  const WindowDecodePlan d = window_decode_plan(p, w.Lmax, w.window, w.n_sink);
+  WinDecodeParams a;
+  a.w = w;
+  a.g_log2 = 0;
+  while ((1 << a.g_log2) < w.G) ++a.g_log2;
+  a.per_chunk = d.per_chunk;
+  a.chunks = d.chunks;
+  a.part_o = static_cast<float*>(ws);
+  const size_t rows = static_cast<size_t>(w.B) * w.Hq * d.chunks;
+  a.part_lse = a.part_o + (d.chunks > 1 ? rows * kHeadDim : 0);
+  const uint64_t items = static_cast<uint64_t>(w.B) * w.Hkv;
+  const uint64_t sinks = static_cast<uint64_t>(std::max(1, std::min(w.n_sink, w.Lmax)));
+  if (items * d.chunks > 0x7fffffffULL) return INFLLMV2_ERR_UNSUPPORTED;
+  CUtensorMap tk, tv, tks, tvs;
+  if (!make_kv_map_3d(&tk, w.k, items, w.Lmax, w.Lmax) || !make_kv_map_3d(&tv, w.v, items, w.Lmax, w.Lmax) ||
+      !make_kv_map_3d(&tks, w.k, items, sinks, w.Lmax) || !make_kv_map_3d(&tvs, w.v, items, sinks, w.Lmax))
+    return INFLLMV2_ERR_CUDA;
+  const size_t smem = window_decode_smem_bytes();
+  int st = set_smem(reinterpret_cast<const void*>(window_decode_kernel), smem);
+  if (st != INFLLMV2_OK) return st;
+  st = launch_pdl(window_decode_kernel, static_cast<unsigned>(items * d.chunks), kWdThreads, smem, s, tk, tv, tks, tvs, a);
+  if (st != INFLLMV2_OK || d.chunks == 1) return st;
+  return launch_pdl(window_decode_merge_kernel, static_cast<unsigned>(w.B * w.Hq), 128, 0, s, a);
 }
 
 // Backward of the window attention (the workspace has window_bwd_plan's layout).
@@ -1226,9 +1289,7 @@ int infllmv2_window_attn_decode(const infllmv2_params* p, const void* q, const v
   if (need > 0 && (ws == nullptr || ws_bytes < need || !aligned16(ws))) return INFLLMV2_ERR_WORKSPACE;
   a.o = static_cast<__nv_bfloat16*>(o);
   a.lse = lse;
-  const long long rows = static_cast<long long>(a.B) * a.Hq;
-  window_rows_kernel<<<static_cast<unsigned>((rows + 3) / 4), 128, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a, 1);
-  return launch_status();
+  return launch_window_decode(p, a, ws, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int infllmv2_window_attn_backward(const infllmv2_params* p, const void* q, const void* k, const void* v, const void* o,
