@@ -6,6 +6,7 @@
 // the caller's stream.  All device code lives in the included .cuh files.
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstring>
 #include <map>
@@ -154,10 +155,16 @@ constexpr size_t kMaxSmem = 227 * 1024;
 
 int launch_status() { return cudaGetLastError() == cudaSuccess ? INFLLMV2_OK : INFLLMV2_ERR_CUDA; }
 
+constexpr int kMaxCachedDevices = 64;
+
+// Multiprocessors of the current device (looked up once per device).
 int num_sms() {
+  static std::atomic<int> cache[kMaxCachedDevices];
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+  if (dev < kMaxCachedDevices && (n = cache[dev].load(std::memory_order_relaxed)) > 0) return n;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) return 148;
+  if (dev < kMaxCachedDevices) cache[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
@@ -211,6 +218,23 @@ int launch_cluster(void (*kern)(Params...), unsigned grid, int C, int threads, s
   }
   if (cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...) != cudaSuccess) return INFLLMV2_ERR_CUDA;
   return launch_status();
+}
+
+// Launches `kern` so that it may start while the previous kernel on the stream finishes (it
+// calls grid_dependency_wait() before it reads anything that kernel wrote).
+template <typename... Params, typename... Args>
+int launch_pdl(void (*kern)(Params...), dim3 grid, int threads, size_t smem, cudaStream_t s, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...) == cudaSuccess ? INFLLMV2_OK : INFLLMV2_ERR_CUDA;
 }
 
 // Decode work layout.  Each (sequence, kv-head) item's selected blocks are split over
@@ -396,6 +420,11 @@ WindowBwdPlan window_bwd_plan(const infllmv2_params* p, int32_t L, int32_t windo
   return d;
 }
 
+unsigned norm_rope_grid(const infllmv2_params* p, int32_t Lq, int ctas_per_sm, int rounds, NormRopeParams* a);
+// CTAs per SM and waves of the norm-and-rotation kernels (the backward's CTAs leave a row of
+// partial weight gradients each).
+constexpr int kNrCtas = 4, kNrWaves = 32, kNrBwdCtas = 2, kNrBwdWaves = 2;
+
 size_t ws_size(const infllmv2_params* p, int op, int32_t L) {
   if (check_params(p) != INFLLMV2_OK || check_len(L) != INFLLMV2_OK) return static_cast<size_t>(-1);
   switch (op) {
@@ -413,8 +442,10 @@ size_t ws_size(const infllmv2_params* p, int op, int32_t L) {
       const size_t rows = static_cast<size_t>(p->batch) * p->num_kv_heads * d.n_splits * kGroupRows;
       return rows * kHeadDim * sizeof(float) + rows * sizeof(float);
     }
-    case INFLLMV2_OP_QK_NORM_ROPE_BACKWARD:
-      return static_cast<size_t>(kNrMaxParts) * 2 * kHeadDim * sizeof(float);
+    case INFLLMV2_OP_QK_NORM_ROPE_BACKWARD: {
+      NormRopeParams a;
+      return static_cast<size_t>(norm_rope_grid(p, L, kNrBwdCtas, kNrBwdWaves, &a)) * kHeadDim * sizeof(float);
+    }
     case INFLLMV2_OP_WINDOW_ATTN: {
       const WindowPlan d = window_plan(p, L);
       return d.n_splits == 1 ? 0 : static_cast<size_t>(d.items) * d.n_splits * 256 * (kHeadDim + 1) * sizeof(float);
@@ -453,6 +484,7 @@ int norm_rope_args(const infllmv2_params* p, const void* q, int64_t q_stride, co
     return INFLLMV2_ERR_INVALID_ARG;
   const int64_t qn = static_cast<int64_t>(p->num_q_heads) * kHeadDim, kn = static_cast<int64_t>(p->num_kv_heads) * kHeadDim;
   if (q_stride < qn || k_stride < kn || q_stride % 8 != 0 || k_stride % 8 != 0) return INFLLMV2_ERR_INVALID_ARG;
+  if (static_cast<uint64_t>(p->batch) * Lq > 0x7fffffffULL) return INFLLMV2_ERR_UNSUPPORTED;  // 32-bit token numbers
   if (!(eps > 0.f) || !std::isfinite(eps)) return INFLLMV2_ERR_INVALID_ARG;
   if (rot < 16 || rot > kHeadDim || rot % 16 != 0) return INFLLMV2_ERR_INVALID_ARG;
   if ((interleaved != 0 && interleaved != 1) || (weights_fp32 != 0 && weights_fp32 != 1)) return INFLLMV2_ERR_INVALID_ARG;
@@ -477,17 +509,23 @@ int norm_rope_args(const infllmv2_params* p, const void* q, int64_t q_stride, co
   return INFLLMV2_OK;
 }
 
-// Heads of one item and CTAs of the launch: up to 12 heads a half-warp (the table row and the
-// weights are loaded once for them), fewer while the items would leave half-warps of the GPU
-// without work.
-unsigned norm_rope_grid(NormRopeParams& a, int ctas_per_sm) {
-  const long long tokens = static_cast<long long>(a.B) * a.Lq, room = static_cast<long long>(ctas_per_sm) * num_sms();
-  const int H = a.Hq + 2 * a.Hkv;
-  a.chunks = (H + 11) / 12;
-  while (a.chunks < H && tokens * a.chunks * 2 <= room * kNrHalves) a.chunks = std::min(H, 2 * a.chunks);
-  a.heads_per_item = (H + a.chunks - 1) / a.chunks;
-  a.chunks = (H + a.heads_per_item - 1) / a.heads_per_item;
-  return static_cast<unsigned>(std::min<long long>((tokens * a.chunks + kNrHalves - 1) / kNrHalves, room));
+// Heads of one chunk and the launch's grid (0: too large): up to 8 heads a half-warp (the table
+// row and the weights are loaded once for them), fewer while the launch would leave half of the
+// GPU's warps (ctas_per_sm CTAs an SM) without work.  `rounds` bounds the CTAs at that many waves.
+unsigned norm_rope_grid(const infllmv2_params* p, int32_t Lq, int ctas_per_sm, int rounds, NormRopeParams* a) {
+  const long long pairs = (static_cast<long long>(p->batch) * Lq + 1) / 2;
+  const long long room = static_cast<long long>(ctas_per_sm) * num_sms();
+  const int Hq = p->num_q_heads, H2 = 2 * p->num_kv_heads;
+  int heads = 8;
+  for (; heads > 1; heads = (heads + 1) / 2)
+    if (pairs * ((Hq + heads - 1) / heads + (H2 + heads - 1) / heads) * 2 > room * kNrWarps) break;
+  const int qc = (Hq + heads - 1) / heads;  // evened out over the query chunks
+  a->heads = heads == 1 ? 1 : std::max((Hq + qc - 1) / qc, std::min(heads, H2));
+  a->q_chunks = (Hq + a->heads - 1) / a->heads;
+  a->kv_chunks = (H2 + a->heads - 1) / a->heads;
+  const long long chunks = a->q_chunks + a->kv_chunks;
+  const long long x = std::min<long long>((pairs + kNrWarps - 1) / kNrWarps, std::max<long long>(1, rounds * room / chunks));
+  return x * chunks > 0x7fffffffLL ? 0u : static_cast<unsigned>(x * chunks);
 }
 
 // Shared checks and parameters of the window attention calls.
@@ -611,6 +649,17 @@ int select_prefill(const infllmv2_params* p, const void* q, int32_t Lq, const vo
   return launch_status();
 }
 
+// Maps over the sinks alone (rows past them read as zeros); without sinks no segment uses them.
+bool sink_maps(const WinParams& w, const CUtensorMap& tk, const CUtensorMap& tv, CUtensorMap* tks, CUtensorMap* tvs) {
+  if (w.n_sink == 0) {
+    *tks = tk;
+    *tvs = tv;
+    return true;
+  }
+  const uint64_t items = static_cast<uint64_t>(w.B) * w.Hkv, sinks = static_cast<uint64_t>(std::min(w.n_sink, w.Lmax));
+  return make_kv_map_3d(tks, w.k, items, sinks, w.Lmax) && make_kv_map_3d(tvs, w.v, items, sinks, w.Lmax);
+}
+
 // Forward of the window attention on the tensor cores.
 int launch_window(const infllmv2_params* p, const WinParams& w, void* ws, cudaStream_t s) {
   const WindowPlan d = window_plan(p, w.Lq);
@@ -623,11 +672,10 @@ int launch_window(const infllmv2_params* p, const WinParams& w, void* ws, cudaSt
   a.part_o = static_cast<float*>(ws);
   a.part_lse = d.n_splits > 1 ? a.part_o + static_cast<size_t>(d.items) * d.n_splits * 256 * kHeadDim : nullptr;
   const uint64_t items = static_cast<uint64_t>(w.B) * w.Hkv;
-  const uint64_t sinks = static_cast<uint64_t>(std::max(1, std::min(w.n_sink, w.Lmax)));
   CUtensorMap tq, tk, tv, tks, tvs;
   if (!make_q_map_3d(&tq, w.q, static_cast<uint64_t>(w.B) * w.Lq, w.Hq, w.G) ||
       !make_kv_map_3d(&tk, w.k, items, w.Lmax, w.Lmax) || !make_kv_map_3d(&tv, w.v, items, w.Lmax, w.Lmax) ||
-      !make_kv_map_3d(&tks, w.k, items, sinks, w.Lmax) || !make_kv_map_3d(&tvs, w.v, items, sinks, w.Lmax))
+      !sink_maps(w, tk, tv, &tks, &tvs))
     return INFLLMV2_ERR_CUDA;
   const size_t smem = window_tc_smem_bytes();
   int st = set_smem(reinterpret_cast<const void*>(window_tc_kernel), smem);
@@ -637,23 +685,6 @@ int launch_window(const infllmv2_params* p, const WinParams& w, void* ws, cudaSt
   const long long rows = static_cast<long long>(w.B) * w.Lq * w.Hq;
   window_merge_kernel<<<static_cast<unsigned>((rows + 7) / 8), 256, 0, s>>>(a);
   return launch_status();
-}
-
-// Launches `kern` so that it may start while the previous kernel on the stream finishes (it
-// calls grid_dependency_wait() before it reads anything that kernel wrote).
-template <typename... Params, typename... Args>
-int launch_pdl(void (*kern)(Params...), unsigned grid, int threads, size_t smem, cudaStream_t s, Args&&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...) == cudaSuccess ? INFLLMV2_OK : INFLLMV2_ERR_CUDA;
 }
 
 int launch_window_decode(const infllmv2_params* p, const WinParams& w, void* ws, cudaStream_t s) {
@@ -668,11 +699,10 @@ int launch_window_decode(const infllmv2_params* p, const WinParams& w, void* ws,
   const size_t rows = static_cast<size_t>(w.B) * w.Hq * d.chunks;
   a.part_lse = a.part_o + (d.chunks > 1 ? rows * kHeadDim : 0);
   const uint64_t items = static_cast<uint64_t>(w.B) * w.Hkv;
-  const uint64_t sinks = static_cast<uint64_t>(std::max(1, std::min(w.n_sink, w.Lmax)));
   if (items * d.chunks > 0x7fffffffULL) return INFLLMV2_ERR_UNSUPPORTED;
   CUtensorMap tk, tv, tks, tvs;
   if (!make_kv_map_3d(&tk, w.k, items, w.Lmax, w.Lmax) || !make_kv_map_3d(&tv, w.v, items, w.Lmax, w.Lmax) ||
-      !make_kv_map_3d(&tks, w.k, items, sinks, w.Lmax) || !make_kv_map_3d(&tvs, w.v, items, sinks, w.Lmax))
+      !sink_maps(w, tk, tv, &tks, &tvs))
     return INFLLMV2_ERR_CUDA;
   const size_t smem = window_decode_smem_bytes();
   int st = set_smem(reinterpret_cast<const void*>(window_decode_kernel), smem);
@@ -701,11 +731,10 @@ int launch_window_backward(const infllmv2_params* p, const WinParams& w, void* w
   a.q_tiles = d.q_tiles;
   a.row_tiles = (w.Lq * w.G + 127) / 128;
   const uint64_t items = static_cast<uint64_t>(w.B) * w.Hkv;
-  const uint64_t sinks = static_cast<uint64_t>(std::max(1, std::min(w.n_sink, w.Lmax)));
   CUtensorMap tq, tdo, tk, tv, tks, tvs;
   if (!make_q_map_4d(&tq, w.q, w.B, w.Lq, w.Hq, w.G) || !make_q_map_4d(&tdo, w.d_o, w.B, w.Lq, w.Hq, w.G) ||
       !make_kv_map_3d(&tk, w.k, items, w.Lmax, w.Lmax) || !make_kv_map_3d(&tv, w.v, items, w.Lmax, w.Lmax) ||
-      !make_kv_map_3d(&tks, w.k, items, sinks, w.Lmax) || !make_kv_map_3d(&tvs, w.v, items, sinks, w.Lmax))
+      !sink_maps(w, tk, tv, &tks, &tvs))
     return INFLLMV2_ERR_CUDA;
   const size_t smem = window_bwd_smem_bytes();
   int st;
@@ -1214,13 +1243,11 @@ int infllmv2_qk_norm_rope(const infllmv2_params* p, const void* q, int64_t q_str
   a.Lout = Lout;
   a.at_position = at_position;
   a.lens_out = lens_out;
-  const unsigned grid = norm_rope_grid(a, 4);
+  const unsigned grid = norm_rope_grid(p, Lq, kNrCtas, kNrWaves, &a);
+  if (grid == 0) return INFLLMV2_ERR_UNSUPPORTED;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (interleaved)
-    qk_norm_rope_kernel<true><<<grid, kNrThreads, 0, s>>>(a);
-  else
-    qk_norm_rope_kernel<false><<<grid, kNrThreads, 0, s>>>(a);
-  return launch_status();
+  return interleaved ? launch_pdl(qk_norm_rope_kernel<true>, grid, kNrThreads, 0, s, a)
+                     : launch_pdl(qk_norm_rope_kernel<false>, grid, kNrThreads, 0, s, a);
 }
 
 int infllmv2_qk_norm_rope_backward(const infllmv2_params* p, const void* q, int64_t q_stride, const void* k,
@@ -1253,15 +1280,17 @@ int infllmv2_qk_norm_rope_backward(const infllmv2_params* p, const void* q, int6
   a.dk_stride = dk_stride;
   a.dv_stride = dv_stride;
   a.part = static_cast<float*>(ws);
-  const unsigned grid = std::min<unsigned>(norm_rope_grid(a, 4), kNrMaxParts);
+  const unsigned grid = norm_rope_grid(p, Lq, kNrBwdCtas, kNrBwdWaves, &a);
+  if (grid == 0) return INFLLMV2_ERR_UNSUPPORTED;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (interleaved)
     qk_norm_rope_bwd_kernel<true><<<grid, kNrThreads, 0, s>>>(a);
   else
     qk_norm_rope_bwd_kernel<false><<<grid, kNrThreads, 0, s>>>(a);
-  if ((st = launch_status()) != INFLLMV2_OK) return st;
-  if (d_qw || d_kw) qk_norm_rope_bwd_weights_kernel<<<8, 1024, 0, s>>>(a.part, static_cast<int>(grid), d_qw, d_kw);
-  return launch_status();
+  if ((st = launch_status()) != INFLLMV2_OK || (!d_qw && !d_kw)) return st;
+  const int each = static_cast<int>(grid) / (a.q_chunks + a.kv_chunks);
+  return launch_pdl(qk_norm_rope_bwd_weights_kernel, dim3(8), 1024, 0, s, a.part, a.q_chunks * each,
+                    a.kv_chunks * each, d_qw, d_kw);
 }
 
 int infllmv2_window_attn(const infllmv2_params* p, const void* q, int32_t Lq, const void* k, const void* v,

@@ -10,11 +10,16 @@
 // Everything is fp32 in registers, rounded once to bf16 on the way out.
 //
 // Both passes are bound by HBM: each head row is read once and written once (256 bytes each
-// way).  A half-warp holds a row (a lane 8 values: one 16-byte load), so the norm is four
-// shuffles and a rotation's partner is in the same lane (interleaved pairs) or one shuffle
-// away (pairs rot / 2 apart; rot is a multiple of 16, so partners sit in the same place of
-// two lanes).  A half-warp takes several heads of one token, so the token's row of the table
-// and the weights are in registers for all of them, with four rows in flight.
+// way).  A half-warp holds a row, a lane two runs of 4 values that are each other's rotation
+// partners (rot / 2 apart, or adjacent for interleaved pairs), so a rotation needs no shuffle
+// and 4 cosines and sines a lane; the norm is four shuffles.  A half-warp takes several heads
+// of one token (all queries, or keys then values), so the token's row of the table and one
+// weight vector stay in registers, with kNrRows rows in flight; the arithmetic is packed in
+// pairs (f32x2), since with one value an instruction the issue slots, not HBM, would bound it.
+// Measured on a 128K prompt, 32 / 2 heads, 2.48 GB: 412 us (0.92 of the measured copy bandwidth);
+// 12 heads an item 442, six rows in flight at two CTAs an SM 526, one wave of CTAs (the short key
+// and value items then leave their SMs early) 477 to 806.  Backward, 2 x 8191 tokens, 449 MB:
+// 111 us (0.61); two rows in flight at three CTAs an SM 121.
 #pragma once
 #include "append.cuh"
 #include "common.cuh"
@@ -22,9 +27,9 @@
 namespace infllmv2 {
 
 constexpr int kNrThreads = 256;
-constexpr int kNrHalves = kNrThreads / 16;  // half-warps of a CTA
-constexpr int kNrUnroll = 4;                // head rows in flight per half-warp
-constexpr int kNrMaxParts = 1024;           // CTAs of the backward at most (rows of d_w partials)
+constexpr int kNrWarps = kNrThreads / 32;
+constexpr int kNrRows = 4;       // head rows in flight per half-warp, forward
+constexpr int kNrBwdRows = 4;    // backward (two loads a row)
 
 struct NormRopeParams {
   const __nv_bfloat16 *q, *k, *v;        // token rows
@@ -36,288 +41,344 @@ struct NormRopeParams {
   int32_t* lens_out;
   const __nv_bfloat16 *dq, *dk, *dv;     // backward: gradients in the attention's layouts
   long long dq_stride, dk_stride, dv_stride;
-  float* part;                           // backward: [grid][2][128] partial d_w
+  float* part;                           // backward: [chunk][CTA of it][128] partial d_w
   int B, Lq, Hq, Hkv, Lout, at_position, weights_fp32, table_rows, rot;
-  int heads_per_item, chunks;            // heads of one item, items of one token
+  int heads, q_chunks, kv_chunks;        // heads of one chunk; grid = chunks * CTAs of a chunk
   float eps;
 };
 
+// Packed pairs of floats.
+__device__ __forceinline__ uint64_t f2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unf2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t swap2(uint64_t v) {
+  float a, b;
+  unf2(v, a, b);
+  return f2(b, a);
+}
+
+// A lane's 8 values of a row: pairs 0, 1 are its first run of 4, pairs 2, 3 the second.
 struct Row8 {
-  float v[8];
+  uint64_t v[4];
+};
+struct Raw8 {
+  uint2 a, b;
 };
 
-__device__ __forceinline__ Row8 unpack8(const uint4& u) {
-  Row8 r;
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    r.v[2 * i] = __uint_as_float(w[i] << 16);
-    r.v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-  return r;
+__device__ __forceinline__ uint64_t unpack_pair(uint32_t u) {
+  return f2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
-__device__ __forceinline__ uint4 pack8(const Row8& r) {
-  return make_uint4(pack_bf16(r.v[0], r.v[1]), pack_bf16(r.v[2], r.v[3]), pack_bf16(r.v[4], r.v[5]),
-                    pack_bf16(r.v[6], r.v[7]));
+__device__ __forceinline__ uint32_t pack_pair(uint64_t v) {
+  float a, b;
+  unf2(v, a, b);
+  return pack_bf16(a, b);
 }
-
-__device__ __forceinline__ Row8 load_weights(const void* w, int fp32, int l) {
-  Row8 r;
-  if (w == nullptr) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) r.v[i] = 1.f;
-  } else if (fp32) {
-    const float4 a = __ldg(static_cast<const float4*>(w) + 2 * l), b = __ldg(static_cast<const float4*>(w) + 2 * l + 1);
-    r.v[0] = a.x, r.v[1] = a.y, r.v[2] = a.z, r.v[3] = a.w;
-    r.v[4] = b.x, r.v[5] = b.y, r.v[6] = b.z, r.v[7] = b.w;
-  } else {
-    r = unpack8(__ldg(static_cast<const uint4*>(w) + l));
-  }
-  return r;
+__device__ __forceinline__ Row8 unpack8(const Raw8& r) {
+  return {{unpack_pair(r.a.x), unpack_pair(r.a.y), unpack_pair(r.b.x), unpack_pair(r.b.y)}};
+}
+__device__ __forceinline__ Raw8 pack8(const Row8& y) {
+  return {make_uint2(pack_pair(y.v[0]), pack_pair(y.v[1])), make_uint2(pack_pair(y.v[2]), pack_pair(y.v[3]))};
 }
 
-// This lane's cosines and sines of table row `t`: of its 8 dimensions (pairs rot / 2 apart)
-// or of its 4 pairs (interleaved; the first four entries).
+// First elements of the lane's two runs.
 template <bool kInterleaved>
-__device__ __forceinline__ void load_angles(const float* table, int rot, int t, int l, Row8& c, Row8& s) {
-  const float* row = table + static_cast<size_t>(t) * rot;
-  if (8 * l >= rot) return;
+__device__ __forceinline__ void lane_runs(int rot, int l, int& a, int& b) {
   if (kInterleaved) {
-    const float4 a = __ldg(reinterpret_cast<const float4*>(row + 4 * l));
-    const float4 b = __ldg(reinterpret_cast<const float4*>(row + rot / 2 + 4 * l));
-    c.v[0] = a.x, c.v[1] = a.y, c.v[2] = a.z, c.v[3] = a.w;
-    s.v[0] = b.x, s.v[1] = b.y, s.v[2] = b.z, s.v[3] = b.w;
-  } else {
-    const int m = rot / 16, i = 8 * (l < m ? l : l - m);
-    const float sg = l < m ? -1.f : 1.f;  // y_a takes -s y_b, y_b takes +s y_a
+    a = 8 * l, b = 8 * l + 4;
+  } else if (l < rot / 8) {
+    a = 4 * l, b = rot / 2 + 4 * l;
+  } else {  // past the rotated dimensions
+    a = 8 * l, b = 8 * l + 4;
+  }
+}
+
+__device__ __forceinline__ Raw8 load_row(const __nv_bfloat16* row, int a, int b) {
+  return {*reinterpret_cast<const uint2*>(row + a), *reinterpret_cast<const uint2*>(row + b)};
+}
+__device__ __forceinline__ void store_row(__nv_bfloat16* row, int a, int b, const Raw8& r) {
+  *reinterpret_cast<uint2*>(row + a) = r.a;
+  *reinterpret_cast<uint2*>(row + b) = r.b;
+}
+
+__device__ __forceinline__ Row8 load_weights(const void* w, int fp32, int a, int b) {
+  if (w == nullptr) {
+    const uint64_t one = f2(1.f, 1.f);
+    return {{one, one, one, one}};
+  }
+  if (!fp32) return unpack8(load_row(static_cast<const __nv_bfloat16*>(w), a, b));
+  const float4 x = *reinterpret_cast<const float4*>(static_cast<const float*>(w) + a);
+  const float4 y = *reinterpret_cast<const float4*>(static_cast<const float*>(w) + b);
+  return {{f2(x.x, x.y), f2(x.z, x.w), f2(y.x, y.y), f2(y.z, y.w)}};
+}
+
+// Cosines and sines of the lane's four rotation pairs at table row t (1 and 0 past rot).
+__device__ __forceinline__ void load_angles(const float* table, int rot, int t, int l, float (&c)[4], float (&s)[4]) {
+  if (8 * l >= rot) return;
+  const float* row = table + static_cast<size_t>(t) * rot + 4 * l;
+  const float4 x = *reinterpret_cast<const float4*>(row), y = *reinterpret_cast<const float4*>(row + rot / 2);
+  c[0] = x.x, c[1] = x.y, c[2] = x.z, c[3] = x.w;
+  s[0] = y.x, s[1] = y.y, s[2] = y.z, s[3] = y.w;
+}
+
+// Rotation by the lane's angles, in packed pairs.  Pairs rot / 2 apart: (a, b) = (a c - b s,
+// a s + b c) run by run.  Interleaved: (x0, x1) = (x0, x1) (c, c) + (x1, x0) (-s, s).
+template <bool kInterleaved>
+struct Turn {
+  uint64_t c[kInterleaved ? 4 : 2], s[kInterleaved ? 4 : 2];
+  __device__ __forceinline__ void set(const float (&cs)[4], const float (&sn)[4], float sign) {
+    if (kInterleaved) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float4 a = __ldg(reinterpret_cast<const float4*>(row + i + 4 * h));
-      const float4 b = __ldg(reinterpret_cast<const float4*>(row + rot / 2 + i + 4 * h));
-      c.v[4 * h] = a.x, c.v[4 * h + 1] = a.y, c.v[4 * h + 2] = a.z, c.v[4 * h + 3] = a.w;
-      s.v[4 * h] = sg * b.x, s.v[4 * h + 1] = sg * b.y, s.v[4 * h + 2] = sg * b.z, s.v[4 * h + 3] = sg * b.w;
+      for (int i = 0; i < 4; ++i) c[i] = f2(cs[i], cs[i]), s[i] = f2(-sign * sn[i], sign * sn[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        c[i] = f2(cs[2 * i], cs[2 * i + 1]), s[i] = f2(sign * sn[2 * i], sign * sn[2 * i + 1]);
     }
   }
-}
-
-// Rotates this lane's 8 values by the angles (kBack: by their negatives).  Called by whole
-// half-warps.
-template <bool kInterleaved, bool kBack>
-__device__ __forceinline__ void rotate(Row8& y, const Row8& c, const Row8& s, int rot, int l) {
-  if (kInterleaved) {
-    if (8 * l < rot) {
+  __device__ __forceinline__ void apply(Row8& y) const {
+    if (kInterleaved) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a = y.v[2 * i], b = y.v[2 * i + 1], sn = kBack ? -s.v[i] : s.v[i];
-        y.v[2 * i] = fmaf(a, c.v[i], -b * sn);
-        y.v[2 * i + 1] = fmaf(a, sn, b * c.v[i]);
+      for (int i = 0; i < 4; ++i) y.v[i] = fma2(y.v[i], c[i], mul2(swap2(y.v[i]), s[i]));
+    } else {
+      const uint64_t neg = f2(-1.f, -1.f);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint64_t a = y.v[i], b = y.v[i + 2];
+        y.v[i] = fma2(a, c[i], mul2(mul2(b, s[i]), neg));
+        y.v[i + 2] = fma2(a, s[i], mul2(b, c[i]));
       }
     }
-  } else {
-    const int m = rot / 16;
-    const int src = l < m ? l + m : (l < 2 * m ? l - m : l);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float o = __shfl_sync(0xffffffffu, y.v[i], src, 16);
-      if (l < 2 * m) y.v[i] = fmaf(y.v[i], c.v[i], o * (kBack ? -s.v[i] : s.v[i]));
-    }
   }
-}
+};
 
 __device__ __forceinline__ float half_sum(float x) {
 #pragma unroll
   for (int d = 8; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d, 16);
   return x;
 }
-
-// The item's sequence: its rows and first position; false (all its rows are left alone) when
-// the rows leave the table or the caches.
-__device__ __forceinline__ bool norm_rope_seq(const NormRopeParams& p, int b, int& n, int& t0) {
-  t0 = p.starts ? p.starts[b] : 0;
-  n = p.q_lens ? min(max(p.q_lens[b], 0), p.Lq) : p.Lq;
-  const long long end = static_cast<long long>(t0) + n;
-  return t0 >= 0 && end <= p.table_rows && (!p.at_position || end <= p.Lout);
+__device__ __forceinline__ float dot8(const Row8& x, const Row8& y) {
+  float a, b;
+  unf2(fma2(x.v[0], y.v[0], mul2(x.v[1], y.v[1])), a, b);
+  float c, d;
+  unf2(fma2(x.v[2], y.v[2], mul2(x.v[3], y.v[3])), c, d);
+  return (a + b) + (c + d);
 }
 
-// Grid-stride over (token, chunk of heads) items, one per half-warp; head h < Hq is a query
-// head, then Hkv key heads, then Hkv value heads.
+// A half-warp's token: sequence b, row r of it, first position t0; live unless the row is
+// padding or its sequence leaves the table or the caches (then all its rows are left alone).
+struct NormRopeToken {
+  unsigned tok;
+  int b, r, t0, n;
+  bool in, fits, live;
+  __device__ __forceinline__ NormRopeToken(const NormRopeParams& p, unsigned token, unsigned tokens) {
+    in = token < tokens;
+    tok = in ? token : 0;
+    b = static_cast<int>(tok / static_cast<unsigned>(p.Lq));
+    r = static_cast<int>(tok - static_cast<unsigned>(b) * static_cast<unsigned>(p.Lq));
+    t0 = p.starts ? p.starts[b] : 0;
+    n = p.q_lens ? min(max(p.q_lens[b], 0), p.Lq) : p.Lq;
+    const long long end = static_cast<long long>(t0) + n;
+    fits = t0 >= 0 && end <= p.table_rows && (!p.at_position || end <= p.Lout);
+    live = in && fits && r < n;
+  }
+};
+
+// A CTA's chunk of heads (p.heads query heads, or p.heads of the Hkv key and then Hkv value heads)
+// and its place among the chunk's CTAs: the chunks of a token run side by side.
+struct NormRopeChunk {
+  int chunk, h0, h1;
+  unsigned x, ctas;
+  bool isq;
+  __device__ __forceinline__ explicit NormRopeChunk(const NormRopeParams& p) {
+    const unsigned n = p.q_chunks + p.kv_chunks;
+    chunk = static_cast<int>(blockIdx.x % n);
+    x = blockIdx.x / n;
+    ctas = gridDim.x / n;
+    isq = chunk < p.q_chunks;
+    h0 = (isq ? chunk : chunk - p.q_chunks) * p.heads;
+    h1 = min(h0 + p.heads, isq ? p.Hq : 2 * p.Hkv);
+  }
+};
+
+// A warp per two tokens, grid-stride over the chunk's CTAs.
 template <bool kInterleaved>
-__global__ void __launch_bounds__(kNrThreads) qk_norm_rope_kernel(const NormRopeParams p) {
+__global__ void __launch_bounds__(kNrThreads, 4) qk_norm_rope_kernel(const NormRopeParams p) {
   grid_dependency_wait();
   const int l = threadIdx.x & 15;
-  const long long items = static_cast<long long>(p.B) * p.Lq * p.chunks;
-  const Row8 wq = load_weights(p.qw, p.weights_fp32, l), wk = load_weights(p.kw, p.weights_fp32, l);
-  const int H = p.Hq + 2 * p.Hkv;
-  const long long stride = static_cast<long long>(gridDim.x) * kNrHalves;
-  // both halves of a warp run the same number of rounds: shuffles name the whole warp
-  const long long first = static_cast<long long>(blockIdx.x) * kNrHalves + (threadIdx.x >> 5) * 2;
-  for (long long base = first; base < items; base += stride) {
-    const long long it = base + ((threadIdx.x >> 4) & 1);
-    const bool in = it < items;
-    const long long tok = in ? it / p.chunks : 0;
-    const int b = static_cast<int>(tok / p.Lq), r = static_cast<int>(tok - static_cast<long long>(b) * p.Lq);
-    const int h0 = in ? static_cast<int>(it - tok * p.chunks) * p.heads_per_item : 0;
-    int n, t0;
-    const bool fits = norm_rope_seq(p, b, n, t0);
-    if (in && r == 0 && h0 == 0 && l == 0) {
-      if (!fits) atomicOr(&g_device_error, kDevErrCacheFull);
-      if (p.lens_out) p.lens_out[b] = fits ? t0 + n : t0;
+  const unsigned tokens = static_cast<unsigned>(p.B) * static_cast<unsigned>(p.Lq);
+  const NormRopeChunk ch(p);
+  const bool isq = ch.isq;
+  const int h0 = ch.h0, h1 = ch.h1;
+  int ra, rb;
+  lane_runs<kInterleaved>(p.rot, l, ra, rb);
+  const Row8 w = load_weights(isq ? p.qw : p.kw, p.weights_fp32, ra, rb);
+  for (unsigned pair = ch.x * kNrWarps + (threadIdx.x >> 5); pair < (tokens + 1) / 2; pair += ch.ctas * kNrWarps) {
+    const NormRopeToken k(p, 2 * pair + ((threadIdx.x >> 4) & 1), tokens);
+    if (k.in && k.r == 0 && ch.chunk == 0 && l == 0) {
+      if (!k.fits) atomicOr(&g_device_error, kDevErrCacheFull);
+      if (p.lens_out) p.lens_out[k.b] = k.fits ? k.t0 + k.n : k.t0;
     }
-    const bool live = in && fits && r < n;
-    Row8 c, s;
+    float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
+    if (k.live) load_angles(p.table, p.rot, k.t0 + k.r, l, c, s);
+    const __nv_bfloat16* q = p.q + k.tok * p.q_stride;
+    const __nv_bfloat16* ks = p.k + k.tok * p.k_stride;
+    const __nv_bfloat16* vs = p.v + k.tok * p.v_stride - p.Hkv * kHeadDim;
+    __nv_bfloat16* qo = p.q_out + static_cast<size_t>(k.tok) * p.Hq * kHeadDim;
+    const size_t head = static_cast<size_t>(p.Lout) * kHeadDim;
+    const size_t ko = static_cast<size_t>(k.b) * p.Hkv * head + static_cast<size_t>(p.at_position ? k.t0 + k.r : k.r) * kHeadDim;
+    for (int hb = h0; hb < h1; hb += kNrRows) {
+      Raw8 raw[kNrRows];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) c.v[i] = 1.f, s.v[i] = 0.f;
-    if (live) load_angles<kInterleaved>(p.table, p.rot, t0 + r, l, c, s);
-    const int orow = p.at_position ? t0 + r : r;
-    for (int hb = 0; hb < p.heads_per_item; hb += kNrUnroll) {
-      uint4 raw[kNrUnroll];
-#pragma unroll
-      for (int u = 0; u < kNrUnroll; ++u) {
-        const int h = h0 + hb + u;
-        raw[u] = make_uint4(0, 0, 0, 0);
-        if (live && hb + u < p.heads_per_item && h < H) {
-          const __nv_bfloat16* src = h < p.Hq ? p.q + tok * p.q_stride + h * kHeadDim
-                                     : h < p.Hq + p.Hkv
-                                         ? p.k + tok * p.k_stride + (h - p.Hq) * kHeadDim
-                                         : p.v + tok * p.v_stride + (h - p.Hq - p.Hkv) * kHeadDim;
-          raw[u] = *(reinterpret_cast<const uint4*>(src) + l);
-        }
+      for (int u = 0; u < kNrRows; ++u) {
+        const int h = hb + u;
+        raw[u] = {make_uint2(0, 0), make_uint2(0, 0)};
+        if (k.live && h < h1) raw[u] = load_row((isq ? q : h < p.Hkv ? ks : vs) + h * kHeadDim, ra, rb);
       }
+      Turn<kInterleaved> turn;
+      turn.set(c, s, 1.f);
 #pragma unroll
-      for (int u = 0; u < kNrUnroll; ++u) {
-        const int h = h0 + hb + u;
+      for (int u = 0; u < kNrRows; ++u) {
+        const int h = hb + u;
+        if (h >= h1) break;  // the same for the whole CTA
         Row8 y = unpack8(raw[u]);
-        float ss = 0.f;
+        const float rs = rsqrtf(half_sum(dot8(y, y)) * (1.f / kHeadDim) + p.eps);
+        const uint64_t r2 = f2(rs, rs);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(y.v[i], y.v[i], ss);
-        const float rs = rsqrtf(half_sum(ss) * (1.f / kHeadDim) + p.eps);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y.v[i] = y.v[i] * rs * (h < p.Hq ? wq.v[i] : wk.v[i]);
-        rotate<kInterleaved, false>(y, c, s, p.rot, l);
-        if (live && hb + u < p.heads_per_item && h < H) {
-          if (h < p.Hq) {
-            *(reinterpret_cast<uint4*>(p.q_out + (tok * p.Hq + h) * kHeadDim) + l) = pack8(y);
-          } else {
-            const bool isk = h < p.Hq + p.Hkv;
-            const int g = h - p.Hq - (isk ? 0 : p.Hkv);
-            const size_t o = ((static_cast<size_t>(b) * p.Hkv + g) * p.Lout + orow) * kHeadDim;
-            *(reinterpret_cast<uint4*>((isk ? p.k_out : p.v_out) + o) + l) = isk ? pack8(y) : raw[u];
-          }
-        }
+        for (int i = 0; i < 4; ++i) y.v[i] = mul2(mul2(y.v[i], r2), w.v[i]);
+        turn.apply(y);
+        if (!k.live) continue;
+        if (isq)
+          store_row(qo + h * kHeadDim, ra, rb, pack8(y));
+        else if (h < p.Hkv)
+          store_row(p.k_out + ko + h * head, ra, rb, pack8(y));
+        else
+          store_row(p.v_out + ko + (h - p.Hkv) * head, ra, rb, raw[u]);
       }
     }
   }
 }
 
-// The backward over the same items: input gradients, and one row of partial weight gradients
+// The backward over the same chunks: input gradients, and one row of partial weight gradients
 // per CTA (its half-warps' sums added in a fixed order).
 template <bool kInterleaved>
-__global__ void __launch_bounds__(kNrThreads) qk_norm_rope_bwd_kernel(const NormRopeParams p) {
+__global__ void __launch_bounds__(kNrThreads, 2) qk_norm_rope_bwd_kernel(const NormRopeParams p) {
   const int l = threadIdx.x & 15;
-  const long long items = static_cast<long long>(p.B) * p.Lq * p.chunks;
-  const Row8 wq = load_weights(p.qw, p.weights_fp32, l), wk = load_weights(p.kw, p.weights_fp32, l);
-  const int H = p.Hq + 2 * p.Hkv;
-  const long long stride = static_cast<long long>(gridDim.x) * kNrHalves;
-  const long long first = static_cast<long long>(blockIdx.x) * kNrHalves + (threadIdx.x >> 5) * 2;
-  Row8 aq, ak;
+  const unsigned tokens = static_cast<unsigned>(p.B) * static_cast<unsigned>(p.Lq);
+  const NormRopeChunk ch(p);
+  const bool isq = ch.isq;
+  const int h0 = ch.h0, h1 = ch.h1;
+  int ra, rb;
+  lane_runs<kInterleaved>(p.rot, l, ra, rb);
+  const Row8 w = load_weights(isq ? p.qw : p.kw, p.weights_fp32, ra, rb);
+  Row8 acc = {{0, 0, 0, 0}};
+  for (unsigned pair = ch.x * kNrWarps + (threadIdx.x >> 5); pair < (tokens + 1) / 2; pair += ch.ctas * kNrWarps) {
+    const NormRopeToken k(p, 2 * pair + ((threadIdx.x >> 4) & 1), tokens);
+    if (k.in && !k.fits && k.r == 0 && ch.chunk == 0 && l == 0) atomicOr(&g_device_error, kDevErrCacheFull);
+    float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
+    if (k.live) load_angles(p.table, p.rot, k.t0 + k.r, l, c, s);
+    const __nv_bfloat16* x0 = isq ? p.q + k.tok * p.q_stride : p.k + k.tok * p.k_stride;
+    const __nv_bfloat16* gq = p.dq + static_cast<size_t>(k.tok) * p.Hq * kHeadDim;
+    const size_t head = static_cast<size_t>(p.Lq) * kHeadDim;
+    const size_t go = static_cast<size_t>(k.b) * p.Hkv * head + static_cast<size_t>(k.r) * kHeadDim;
+    for (int hb = h0; hb < h1; hb += kNrBwdRows) {
+      Raw8 rx[kNrBwdRows], rg[kNrBwdRows];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) aq.v[i] = ak.v[i] = 0.f;
-  for (long long base = first; base < items; base += stride) {
-    const long long it = base + ((threadIdx.x >> 4) & 1);
-    const bool in = it < items;
-    const long long tok = in ? it / p.chunks : 0;
-    const int b = static_cast<int>(tok / p.Lq), r = static_cast<int>(tok - static_cast<long long>(b) * p.Lq);
-    const int h0 = in ? static_cast<int>(it - tok * p.chunks) * p.heads_per_item : 0;
-    int n, t0;
-    const bool fits = norm_rope_seq(p, b, n, t0);
-    if (in && !fits && r == 0 && h0 == 0 && l == 0) atomicOr(&g_device_error, kDevErrCacheFull);
-    const bool live = in && fits && r < n;
-    Row8 c, s;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) c.v[i] = 1.f, s.v[i] = 0.f;
-    if (live) load_angles<kInterleaved>(p.table, p.rot, t0 + r, l, c, s);
-    for (int hb = 0; hb < p.heads_per_item; hb += 2) {
-      uint4 rx[2], rg[2];
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int h = h0 + hb + u;
-        rx[u] = rg[u] = make_uint4(0, 0, 0, 0);
-        if (live && hb + u < p.heads_per_item && h < H) {
-          if (h < p.Hq) {
-            rx[u] = *(reinterpret_cast<const uint4*>(p.q + tok * p.q_stride + h * kHeadDim) + l);
-            rg[u] = *(reinterpret_cast<const uint4*>(p.dq + (tok * p.Hq + h) * kHeadDim) + l);
-          } else {
-            const bool isk = h < p.Hq + p.Hkv;
-            const int g = h - p.Hq - (isk ? 0 : p.Hkv);
-            const size_t o = ((static_cast<size_t>(b) * p.Hkv + g) * p.Lq + r) * kHeadDim;
-            if (isk) rx[u] = *(reinterpret_cast<const uint4*>(p.k + tok * p.k_stride + g * kHeadDim) + l);
-            rg[u] = *(reinterpret_cast<const uint4*>((isk ? p.dk : p.dv) + o) + l);
-          }
+      for (int u = 0; u < kNrBwdRows; ++u) {
+        const int h = hb + u;
+        rx[u] = rg[u] = {make_uint2(0, 0), make_uint2(0, 0)};
+        if (k.live && h < h1) {
+          if (isq || h < p.Hkv) rx[u] = load_row(x0 + h * kHeadDim, ra, rb);
+          rg[u] = load_row(isq ? gq + h * kHeadDim : h < p.Hkv ? p.dk + go + h * head : p.dv + go + (h - p.Hkv) * head,
+                           ra, rb);
         }
       }
+      Turn<kInterleaved> back;
+      back.set(c, s, -1.f);
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int h = h0 + hb + u;
-        const bool isq = h < p.Hq, isk = !isq && h < p.Hq + p.Hkv;
+      for (int u = 0; u < kNrBwdRows; ++u) {
+        const int h = hb + u;
+        if (h >= h1) break;  // the same for the whole CTA
+        if (!isq && h >= p.Hkv) {
+          if (k.live) store_row(p.v_out + k.tok * p.dv_stride + (h - p.Hkv) * kHeadDim, ra, rb, rg[u]);
+          continue;
+        }
         const Row8 x = unpack8(rx[u]);
         Row8 g = unpack8(rg[u]);
-        rotate<kInterleaved, true>(g, c, s, p.rot, l);
-        float ss = 0.f, dot = 0.f;
+        back.apply(g);
+        Row8 gw;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          ss = fmaf(x.v[i], x.v[i], ss);
-          dot = fmaf(g.v[i] * (isq ? wq.v[i] : wk.v[i]), x.v[i], dot);
-        }
-        ss = half_sum(ss);
-        dot = half_sum(dot);
+        for (int i = 0; i < 4; ++i) gw.v[i] = mul2(g.v[i], w.v[i]);
+        const float ss = half_sum(dot8(x, x)), dot = half_sum(dot8(gw, x));
         const float rs = rsqrtf(ss * (1.f / kHeadDim) + p.eps);
-        const float k3 = rs * rs * rs * dot * (1.f / kHeadDim);
-        if (live && hb + u < p.heads_per_item && h < H) {
-          Row8 dx;
+        const float k3 = -rs * rs * rs * dot * (1.f / kHeadDim);
+        const uint64_t r2 = f2(rs, rs), n3 = f2(k3, k3);
+        Row8 dx;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float w = isq ? wq.v[i] : wk.v[i];
-            const float dw = g.v[i] * x.v[i] * rs;
-            if (isq) aq.v[i] += dw;
-            if (isk) ak.v[i] += dw;
-            dx.v[i] = fmaf(rs * g.v[i], w, -x.v[i] * k3);
-          }
-          __nv_bfloat16* dst = isq   ? p.q_out + tok * p.dq_stride + h * kHeadDim
-                               : isk ? p.k_out + tok * p.dk_stride + (h - p.Hq) * kHeadDim
-                                     : p.v_out + tok * p.dv_stride + (h - p.Hq - p.Hkv) * kHeadDim;
-          *(reinterpret_cast<uint4*>(dst) + l) = isq || isk ? pack8(dx) : rg[u];
+        for (int i = 0; i < 4; ++i) {
+          acc.v[i] = fma2(mul2(g.v[i], r2), x.v[i], acc.v[i]);  // rows that are not live are zeros
+          dx.v[i] = fma2(gw.v[i], r2, mul2(x.v[i], n3));
         }
+        if (k.live)
+          store_row(isq ? p.q_out + k.tok * p.dq_stride + h * kHeadDim : p.k_out + k.tok * p.dk_stride + h * kHeadDim,
+                    ra, rb, pack8(dx));
       }
     }
   }
-  __shared__ float red[kNrHalves][2][kHeadDim];
+  __shared__ float red[2 * kNrWarps][kHeadDim];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    red[threadIdx.x >> 4][0][8 * l + i] = aq.v[i];
-    red[threadIdx.x >> 4][1][8 * l + i] = ak.v[i];
+  for (int i = 0; i < 4; ++i) {
+    const int d = (i < 2 ? ra : rb) + 2 * (i & 1);
+    unf2(acc.v[i], red[threadIdx.x >> 4][d], red[threadIdx.x >> 4][d + 1]);
   }
   __syncthreads();
-  float a = 0.f;
+  if (threadIdx.x < kHeadDim) {
+    float a = 0.f;
 #pragma unroll
-  for (int w = 0; w < kNrHalves; ++w) a += red[w][threadIdx.x >> 7][threadIdx.x & 127];
-  p.part[static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x] = a;
+    for (int i = 0; i < 2 * kNrWarps; ++i) a += red[i][threadIdx.x];
+    p.part[(static_cast<size_t>(ch.chunk) * ch.ctas + ch.x) * kHeadDim + threadIdx.x] = a;
+  }
 }
 
-// d_qw and d_kw from the CTAs' partials: grid 8, a CTA sums 32 of the 256 columns, 32 threads
-// of a column over every 32nd part, then over the threads, in fp64 in a fixed order.
+// d_qw (from the first q_parts rows of partials) and d_kw (from the other k_parts): grid 8, a
+// CTA sums 32 of the 256 columns, 32 threads of a column over every 32nd row, then over the
+// threads, in fp64 in a fixed order.
 __global__ void __launch_bounds__(1024)
-    qk_norm_rope_bwd_weights_kernel(const float* __restrict__ part, int parts, float* __restrict__ d_qw,
-                                    float* __restrict__ d_kw) {
+    qk_norm_rope_bwd_weights_kernel(const float* __restrict__ part, int q_parts, int k_parts,
+                                    float* __restrict__ d_qw, float* __restrict__ d_kw) {
   __shared__ double red[32][33];
-  const int x = threadIdx.x & 31, y = threadIdx.x >> 5, col = blockIdx.x * 32 + x;
+  grid_dependency_wait();
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5, col = (blockIdx.x & 3) * 32 + x;
+  const bool isq = blockIdx.x < 4;
+  if (!isq) part += static_cast<size_t>(q_parts) * kHeadDim;
+  const int parts = isq ? q_parts : k_parts;
   double a = 0.0;
-  for (int i = y; i < parts; i += 32) a += part[static_cast<size_t>(i) * 256 + col];
+  for (int i = y; i < parts; i += 32) a += part[static_cast<size_t>(i) * kHeadDim + col];
   red[y][x] = a;
   __syncthreads();
   if (y == 0) {
     for (int i = 1; i < 32; ++i) a += red[i][x];
-    float* out = col < kHeadDim ? d_qw : d_kw;
-    if (out) out[col & (kHeadDim - 1)] = static_cast<float>(a);
+    float* out = isq ? d_qw : d_kw;
+    if (out) out[col] = static_cast<float>(a);
   }
 }
 

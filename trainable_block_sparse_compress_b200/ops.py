@@ -36,9 +36,14 @@ class Params:
         return self.num_q_heads // self.num_kv_heads
 
     def c(self) -> _lib.CParams:
-        return _lib.CParams(self.batch, self.num_q_heads, self.num_kv_heads, self.head_dim, self.block_size,
-                            self.kernel_size, self.kernel_stride, self.topk, self.n_init, self.n_local,
-                            float(self.softmax_scale), int(self.score_mode), int(self.pool_mode))
+        """The C struct, made once (the fields are frozen; the library only reads it)."""
+        c = self.__dict__.get("_c")
+        if c is None:
+            c = _lib.CParams(self.batch, self.num_q_heads, self.num_kv_heads, self.head_dim, self.block_size,
+                             self.kernel_size, self.kernel_stride, self.topk, self.n_init, self.n_local,
+                             float(self.softmax_scale), int(self.score_mode), int(self.pool_mode))
+            self.__dict__["_c"] = c
+        return c
 
     @staticmethod
     def from_workload(wl, batch: Optional[int] = None) -> "Params":
@@ -61,8 +66,16 @@ def workspace_size(p: Params, op: int, L: int) -> int:
     return v
 
 
-def _stream() -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+# The binding's own time bounds the smallest calls (a decode token's GPU work is a few us), so
+# the current device and stream are read without building torch objects where torch offers it.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream() -> int:
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(_current_device())
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -70,9 +83,12 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _need(t: torch.Tensor, name: str, dtype, shape=None):
+    if (t.is_cuda and t.dtype is dtype and t.is_contiguous() and (shape is None or t.shape == shape)
+            and t.get_device() == _current_device()):
+        return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
+    if t.get_device() != _current_device():
         # the library launches on the current device: another device's pointer is not its memory
         raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
     if t.dtype != dtype:
@@ -323,27 +339,32 @@ def _need_tokens(t: torch.Tensor, name: str, B: int, L: int, H: int, d: int) -> 
     (a slice of a packed projection output is such a view).  Returns that stride."""
     if t.dim() != 4:
         raise ValueError(f"{name} must have 4 dimensions, got {t.dim()}")
-    _need(t[:1, :1], name, torch.bfloat16)  # device and dtype; heads contiguous
     if tuple(t.shape) != (B, L, H, d):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(B, L, H, d)}")
-    # a stride over an axis of length 1 says nothing
+    sb, sl, sh, sd = t.stride()
+    # device and dtype, and each token's heads contiguous (a stride over an axis of length 1 says nothing)
+    if not (t.is_cuda and t.dtype is torch.bfloat16 and sd == 1 and (sh == d or H == 1)
+            and t.get_device() == _current_device()):
+        _need(t[:1, :1], name, torch.bfloat16)
     if L > 1:
-        stride = t.stride(1)
+        stride = sl
     elif B > 1:
-        stride = t.stride(0)
+        stride = sb
     else:
         stride = H * d
-    if B > 1 and t.stride(0) != L * stride:
+    if B > 1 and sb != L * stride:
         raise ValueError(f"{name} must have one stride between consecutive tokens, got {t.stride()}")
     return stride
 
 
 def _norm_weights(p: Params, q_weight, k_weight) -> int:
     """Checks the norm weights ([d], both fp32 or both bf16, each may be None); 1 when fp32."""
-    dtypes = {w.dtype for w in (q_weight, k_weight) if w is not None}
-    if len(dtypes) > 1:
+    first = q_weight if q_weight is not None else k_weight
+    if first is None:
+        return 0
+    dt = first.dtype
+    if k_weight is not None and k_weight.dtype is not dt:
         raise ValueError("q_weight and k_weight must have one dtype")
-    dt = dtypes.pop() if dtypes else torch.bfloat16
     if dt not in (torch.float32, torch.bfloat16):
         raise ValueError(f"q_weight and k_weight must be torch.float32 or torch.bfloat16, got {dt}")
     for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
@@ -380,7 +401,7 @@ def qk_norm_rope(p: Params, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, t
     if (k_cache is None) != (v_cache is None):
         raise ValueError("k_cache and v_cache go together")
     if q_out is None:
-        q_out = torch.empty((B, Lq, p.num_q_heads, p.head_dim), dtype=torch.bfloat16, device=q.device)
+        q_out = q.new_empty((B, Lq, p.num_q_heads, p.head_dim))
     _need(q_out, "q_out", torch.bfloat16, (B, Lq, p.num_q_heads, p.head_dim))
     if k_cache is not None:
         if k_out is not None or v_out is not None:
@@ -389,7 +410,7 @@ def qk_norm_rope(p: Params, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, t
     else:
         Lout = Lq
         if k_out is None:
-            k_out = torch.empty((B, p.num_kv_heads, Lq, p.head_dim), dtype=torch.bfloat16, device=q.device)
+            k_out = q.new_empty((B, p.num_kv_heads, Lq, p.head_dim))
         if v_out is None:
             v_out = torch.empty_like(k_out)
     for t, name in ((k_out, "k_cache" if k_cache is not None else "k_out"),
