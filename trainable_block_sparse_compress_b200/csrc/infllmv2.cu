@@ -738,15 +738,15 @@ int launch_window_backward(const infllmv2_params* p, const WinParams& w, void* w
     return INFLLMV2_ERR_CUDA;
   const size_t smem = window_bwd_smem_bytes();
   int st;
-  if ((st = set_smem(reinterpret_cast<const void*>(window_dkdv_tc_kernel), smem)) != INFLLMV2_OK) return st;
-  if ((st = set_smem(reinterpret_cast<const void*>(window_dq_tc_kernel), smem)) != INFLLMV2_OK) return st;
-  const long long rows = static_cast<long long>(w.B) * a.Lp * w.Hq;
+  if ((st = set_smem(reinterpret_cast<const void*>(window_bwd_tc_kernel), smem)) != INFLLMV2_OK) return st;
+  const long long delta_items = static_cast<long long>(w.B) * a.Lp * ((w.Hq + 3) / 4);
   const long long ctas = static_cast<long long>(items) * (static_cast<long long>(d.sink_tiles) * d.chunks_s +
                                                           static_cast<long long>(d.key_tiles - d.sink_tiles) * d.chunks_w);
   const long long dq_ctas = static_cast<long long>(items) * a.row_tiles;
-  if (ctas > 0x7fffffffLL || dq_ctas > 0x7fffffffLL || items > 65535) return INFLLMV2_ERR_UNSUPPORTED;
-  window_delta_kernel<<<static_cast<unsigned>(std::min<long long>((rows + 15) / 16, 8LL * num_sms())), 256, 0, s>>>(a);
-  window_dkdv_tc_kernel<<<static_cast<unsigned>(ctas), kWbThreads, smem, s>>>(tq, tdo, tk, tv, a);
+  if (delta_items > 0x7fffffffLL || ctas + dq_ctas > 0x7fffffffLL || items > 65535) return INFLLMV2_ERR_UNSUPPORTED;
+  a.kv_items = static_cast<int>(ctas);
+  window_delta_kernel<<<static_cast<unsigned>(std::min<long long>((delta_items + 15) / 16, 64LL * num_sms())), 256, 0, s>>>(a);
+  window_bwd_tc_kernel<<<static_cast<unsigned>(ctas + dq_ctas), kWbThreads, smem, s>>>(tq, tdo, tk, tv, tks, tvs, a);
   if ((st = launch_status()) != INFLLMV2_OK) return st;
   const int first = d.chunks_s > 1 ? 0 : d.sink_tiles;
   const int split = d.chunks_w > 1 ? d.key_tiles - first : (d.chunks_s > 1 ? d.sink_tiles : 0);
@@ -754,7 +754,6 @@ int launch_window_backward(const infllmv2_params* p, const WinParams& w, void* w
     const dim3 grid(static_cast<unsigned>(split) * (2 * kWbKeys / 8), static_cast<unsigned>(items));
     window_dkdv_merge_kernel<<<grid, 256, 0, s>>>(a, first, split);
   }
-  window_dq_tc_kernel<<<static_cast<unsigned>(dq_ctas), kWbThreads, smem, s>>>(tq, tdo, tk, tv, tks, tvs, a);
   return launch_status();
 }
 

@@ -47,30 +47,6 @@ struct NormRopeParams {
   float eps;
 };
 
-// Packed pairs of floats.
-__device__ __forceinline__ uint64_t f2(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void unf2(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 __device__ __forceinline__ uint64_t swap2(uint64_t v) {
   float a, b;
   unf2(v, a, b);
@@ -87,11 +63,6 @@ struct Raw8 {
 
 __device__ __forceinline__ uint64_t unpack_pair(uint32_t u) {
   return f2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
-}
-__device__ __forceinline__ uint32_t pack_pair(uint64_t v) {
-  float a, b;
-  unf2(v, a, b);
-  return pack_bf16(a, b);
 }
 __device__ __forceinline__ Row8 unpack8(const Raw8& r) {
   return {{unpack_pair(r.a.x), unpack_pair(r.a.y), unpack_pair(r.b.x), unpack_pair(r.b.y)}};

@@ -2,15 +2,15 @@
 // the 5th-generation tensor cores.
 //
 // Rows are (token, head of the group) as in the forward: 128 / G tokens x G heads a tile.
-//   window_delta_kernel  D = dO . O and lse in base 2, one value per row, laid out row by row
-//           ([B, Hkv, token, head of the group], tokens padded to 128) so that a tile's 128
-//           values are contiguous; rows past a sequence's end get lse = +inf (P = 0) and D = 0.
-//   window_dkdv_tc_kernel  per 128 keys of a (sequence, kv-head), over the query tiles that see
+//   window_delta_kernel  D = dO . O and lse in base 2, negated, one value per row, laid out row by
+//           row ([B, Hkv, token, head of the group], tokens padded to 128) so that a tile's 128
+//           values are contiguous; rows past a sequence's end get -lse = -inf (P = 0) and D = 0.
+//   window_bwd_tc_kernel, dK / dV items: per 128 keys of a (sequence, kv-head), over the query tiles that see
 //           one of them: S^T = K Q^T and dP^T = V dO^T (keys x rows), P^T = exp2(S^T - lse),
 //           dS^T = P^T (dP^T - D), then dV += P^T dO and dK += dS^T Q with P^T and dS^T as A
 //           operands in TMEM (bf16, written over S^T and dP^T): nothing but the Q / dO tiles
 //           passes through shared memory, and the group's heads are summed in the accumulator.
-//   window_dq_tc_kernel  per 128 rows, over the keys that they see: S = Q K^T, dP = dO V^T,
+//   window_bwd_tc_kernel, dq items: per 128 rows, over the keys that they see: S = Q K^T, dP = dO V^T,
 //           dQ += dS K with dS as the A operand in TMEM.
 // S and dP are computed in both (7 products instead of 5): that keeps dq out of fp32 atomics
 // (its order of sums is fixed) and of a 4-byte accumulator in HBM.
@@ -24,13 +24,15 @@
 
 namespace infllmv2 {
 
-constexpr int kWbThreads = 32 * 10;
-constexpr int kWbTmaWarp = 8, kWbMmaWarp = 9;
+constexpr int kWbGroups = 4;                 // elementwise warpgroups, 32 columns of a tile each
+constexpr int kWbEltWarps = 4 * kWbGroups;
+constexpr int kWbThreads = 32 * (kWbEltWarps + 2);
+constexpr int kWbTmaWarp = kWbEltWarps, kWbMmaWarp = kWbEltWarps + 1;
 constexpr int kWbSlots = 5;
 constexpr int kWbKeys = 128;  // keys of a dK / dV tile
 
 struct WbSmem {
-  uint64_t res_full, full[kWbSlots], empty[kWbSlots], s_full[2], dp_full, p_full[2], ds_full[2], done, mma_done, tail[2];
+  uint64_t res_full, full[kWbSlots], empty[kWbSlots], s_full[2], dp_full, p_full, ds_full, done, mma_done, tail[2];
   uint64_t st_full[2], st_empty[2];
   alignas(16) float stats[2][2][128];  // dK / dV: lse and D of a query tile's rows
   uint32_t tmem_base;
@@ -45,42 +47,52 @@ static_assert(window_bwd_smem_bytes() <= 227 * 1024, "shared memory of one CTA")
 struct WinBwdParams {
   WinParams w;
   int g_log2, Lp;       // Lp: tokens padded to a multiple of 128
-  float *lse2, *delta;  // [B, Hkv, Lp, G]
+  float *lse2, *delta;  // [B, Hkv, Lp, G]: -lse in base 2 and -D
   // dK / dV: key tiles 0 .. sink_tiles-1 have chunks_s chunks of q_tiles query tiles, the others
   // chunks_w; a kind with more than one chunk goes through the partials
   int key_tiles, sink_tiles, chunks_s, chunks_w, q_tiles, row_tiles;
+  int kv_items;         // CTAs of the dK / dV part
   float* part;          // [chunk slot][dV, dK][128 keys][128]
 };
 
-// One half-warp per row (token, q-head): grid-stride over B * Lp * Hq rows.
+// One half-warp per four heads of a token, four rows of O and dO in flight: bound by HBM.
+// grid-stride over B * Lp * ceil(Hq / 4) items, two to a warp.
 __global__ void __launch_bounds__(256) window_delta_kernel(const WinBwdParams p) {
   const WinParams& w = p.w;
   const int l = threadIdx.x & 15;
-  const long long rows = static_cast<long long>(w.B) * p.Lp * w.Hq;
-  const long long stride = static_cast<long long>(gridDim.x) * 16;
-  for (long long base = static_cast<long long>(blockIdx.x) * 16 + (threadIdx.x >> 5) * 2; base < rows; base += stride) {
-    const long long row = base + ((threadIdx.x >> 4) & 1);
-    const int h = static_cast<int>(row % w.Hq), t = static_cast<int>(row / w.Hq % p.Lp);
-    const int b = static_cast<int>(row / w.Hq / p.Lp);
-    const bool in = row < rows && t < chunk_lens(w.q_lens, w.kv_lens, min(b, w.B - 1), w.Lq, w.Lmax).q_len;
-    float s = 0.f;
-    if (in) {
-      const size_t o = ((static_cast<size_t>(b) * w.Lq + t) * w.Hq + h) * kHeadDim;
-      const uint4 ua = *(reinterpret_cast<const uint4*>(w.o_in + o) + l);
-      const uint4 ub = *(reinterpret_cast<const uint4*>(w.d_o + o) + l);
-      const uint32_t xa[4] = {ua.x, ua.y, ua.z, ua.w}, xb[4] = {ub.x, ub.y, ub.z, ub.w};
+  const unsigned groups = (static_cast<unsigned>(w.Hq) + 3) / 4, items = static_cast<unsigned>(w.B) * p.Lp * groups;
+  for (unsigned base = blockIdx.x * 16 + (threadIdx.x >> 5) * 2; base < items; base += gridDim.x * 16) {
+    const unsigned it = min(base + ((threadIdx.x >> 4) & 1), items - 1);  // an odd count: the last twice
+    const unsigned tok = it / groups, b = tok / static_cast<unsigned>(p.Lp);
+    const int h0 = static_cast<int>(it - tok * groups) * 4, t = static_cast<int>(tok - b * p.Lp);
+    const bool in = t < chunk_lens(w.q_lens, w.kv_lens, static_cast<int>(b), w.Lq, w.Lmax).q_len;
+    const size_t o = ((static_cast<size_t>(b) * w.Lq + t) * w.Hq + h0) * kHeadDim;
+    uint4 x[4], y[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      x[u] = y[u] = make_uint4(0, 0, 0, 0);
+      if (in && h0 + u < w.Hq) {
+        x[u] = *(reinterpret_cast<const uint4*>(w.o_in + o + u * kHeadDim) + l);
+        y[u] = *(reinterpret_cast<const uint4*>(w.d_o + o + u * kHeadDim) + l);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const uint32_t xa[4] = {x[u].x, x[u].y, x[u].z, x[u].w}, xb[4] = {y[u].x, y[u].y, y[u].z, y[u].w};
+      float s = 0.f;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         s = fmaf(__uint_as_float(xa[i] << 16), __uint_as_float(xb[i] << 16), s);
         s = fmaf(__uint_as_float(xa[i] & 0xffff0000u), __uint_as_float(xb[i] & 0xffff0000u), s);
       }
-    }
 #pragma unroll
-    for (int d = 8; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d, 16);
-    if (row < rows && l == 0) {
-      const size_t i = ((static_cast<size_t>(b) * w.Hkv + (h >> p.g_log2)) * p.Lp + t) * w.G + (h & (w.G - 1));
-      p.lse2[i] = in ? w.lse[(static_cast<size_t>(b) * w.Hq + h) * w.Lq + t] * 1.4426950408889634f : INFINITY;
-      p.delta[i] = s;
+      for (int d = 8; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d, 16);
+      const int h = h0 + u;
+      if (l == 0 && h < w.Hq) {
+        const size_t i = ((static_cast<size_t>(b) * w.Hkv + (h >> p.g_log2)) * p.Lp + t) * w.G + (h & (w.G - 1));
+        p.lse2[i] = in ? w.lse[(static_cast<size_t>(b) * w.Hq + h) * w.Lq + t] * -1.4426950408889634f : -INFINITY;
+        p.delta[i] = -s;
+      }
     }
   }
 }
@@ -108,6 +120,26 @@ __device__ __forceinline__ int window_t_end(const WinParams& w, int i, int len) 
   return static_cast<int>(min(static_cast<long long>(len), static_cast<long long>(i) * kWbKeys + kWbKeys - 1 + w.window));
 }
 
+// 16 columns of this thread's TMEM lane, without the wait (tmem_wait_st follows).
+__device__ __forceinline__ void tmem_st16_nowait(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+// Zeroes the values of 16 pairs whose bit (0..31) is not set.
+__device__ __forceinline__ void mask_pairs(uint64_t (&v)[16], uint32_t bits) {
+#pragma unroll
+  for (int q = 0; q < 16; ++q) {
+    float a, b;
+    unf2(v[q], a, b);
+    v[q] = f2((bits >> (2 * q)) & 1u ? a : 0.f, (bits >> (2 * q + 1)) & 1u ? b : 0.f);
+  }
+}
+
 // S or dP products: D[tmem] = A[128 rows] * B[128 rows]^T over the 128 head dimensions.
 __device__ __forceinline__ void umma_rows(uint32_t d, uint32_t a, uint32_t b) {
   constexpr uint32_t id = idesc_bf16_f32(128, 128, false, false);
@@ -117,31 +149,29 @@ __device__ __forceinline__ void umma_rows(uint32_t d, uint32_t a, uint32_t b) {
     umma_bf16(d, desc_k_sw128(a + o), desc_k_sw128(b + o), id, k > 0 ? 1u : 0u);
   }
 }
-// D[tmem] += A[tmem] * B: A holds 64 values of K in the first 32 columns of each of its two
-// 64-column halves, B's 128 rows are the K axis.
+// D[tmem] += A[tmem] * B: A holds 32 values of K in the first 16 columns of each of its four
+// 32-column quarters (a warpgroup writes its quarter over what it has read), B's 128 rows are
+// the K axis.
 __device__ __forceinline__ void umma_acc(uint32_t d, uint32_t a, uint32_t b, bool first) {
   constexpr uint32_t id = idesc_bf16_f32(128, 128, false, true);
 #pragma unroll
   for (int k = 0; k < 8; ++k)
-    umma_bf16_ta(d, a + 64u * (k >> 2) + 8u * (k & 3), desc_mn_sw128(b + k * 2048, kWfHalf, 1024), id,
+    umma_bf16_ta(d, a + 32u * (k >> 1) + 8u * (k & 1), desc_mn_sw128(b + k * 2048, kWfHalf, 1024), id,
                  (!first || k > 0) ? 1u : 0u);
 }
 
-// grid = B * Hkv * (sink_tiles * chunks_s + (key_tiles - sink_tiles) * chunks_w).
-// TMEM: S^T 0, dP^T 128, dV 256, dK 384.
-__global__ void __launch_bounds__(kWbThreads, 1)
-    window_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
-                          const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                          const WinBwdParams p) {
-  extern __shared__ __align__(1024) unsigned char smem_1k[];
-  unsigned char* base = smem_1k;
+// One dK / dV item: `cta` of B * Hkv * (sink_tiles * chunks_s + (key_tiles - sink_tiles) *
+// chunks_w).  TMEM: S^T 0, dP^T 128, dV 256, dK 384.
+__device__ __forceinline__ void window_dkdv(const CUtensorMap& tm_q, const CUtensorMap& tm_do, const CUtensorMap& tm_k,
+                                            const CUtensorMap& tm_v, const WinBwdParams& p, unsigned char* base,
+                                            int cta) {
   unsigned char* kv = base;                        // K tile, V tile
   unsigned char* ring = base + 2 * kWfTileBytes;   // Q / dO slots: Q0 dO0 Q1 dO1 ...
   WbSmem& S = *reinterpret_cast<WbSmem*>(ring + kWbSlots * kWfTileBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const WinParams& w = p.w;
 
-  const int bg = blockIdx.x % (w.B * w.Hkv), e = blockIdx.x / (w.B * w.Hkv);
+  const int bg = cta % (w.B * w.Hkv), e = cta / (w.B * w.Hkv);
   const bool sink_kind = e < p.sink_tiles * p.chunks_s;
   const int chunks = sink_kind ? p.chunks_s : p.chunks_w;
   const int e2 = sink_kind ? e : e - p.sink_tiles * p.chunks_s;
@@ -166,12 +196,12 @@ __global__ void __launch_bounds__(kWbThreads, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&S.s_full[s], 1);
-      mbar_init(&S.p_full[s], 4);
-      mbar_init(&S.ds_full[s], 4);
       mbar_init(&S.tail[s], 1);
       mbar_init(&S.st_full[s], 1);
-      mbar_init(&S.st_empty[s], 8);
+      mbar_init(&S.st_empty[s], kWbEltWarps);
     }
+    mbar_init(&S.p_full, kWbEltWarps);
+    mbar_init(&S.ds_full, kWbEltWarps);
     mbar_init(&S.dp_full, 1);
     mbar_init(&S.done, 1);
     mbar_init(&S.mma_done, 1);
@@ -274,8 +304,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
         umma_commit(&S.dp_full);
       }
       for (int i = 0; i < n && ok; ++i) {
-        for (int h = 0; h < 2 && ok; ++h) ok = mbar_wait(&S.p_full[h], i & 1u, &S.abort);
-        if (!ok) break;
+        if (!mbar_wait(&S.p_full, i & 1u, &S.abort)) break;
         tc_fence_after();
         umma_acc(tmem + 256, tmem, at(2 * i + 1), i == 0);
         umma_commit(&S.empty[(2 * i + 1) % kWbSlots]);
@@ -284,8 +313,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
           umma_rows(tmem, ka, at(2 * i + 2));
           umma_commit(&S.s_full[0]);
         }
-        for (int h = 0; h < 2 && ok; ++h) ok = mbar_wait(&S.ds_full[h], i & 1u, &S.abort);
-        if (!ok) break;
+        if (!mbar_wait(&S.ds_full, i & 1u, &S.abort)) break;
         tc_fence_after();
         umma_acc(tmem + 384, tmem + 128, at(2 * i), i == 0);
         umma_commit(&S.empty[(2 * i) % kWbSlots]);
@@ -299,7 +327,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
       umma_commit(&S.mma_done);
     }
     __syncwarp();
-    named_bar_sync(1, 32 * 9);
+    named_bar_sync(1, 32 * (kWbEltWarps + 1));
     if (lane == 0) mbar_wait_drain(&S.mma_done, 0);
     __syncwarp();
     tc_fence_after();
@@ -307,103 +335,98 @@ __global__ void __launch_bounds__(kWbThreads, 1)
     return;
   }
 
-  // ---------------------------------------- elementwise: thread = key, a warpgroup half the rows
+  // ------------------------------- elementwise: thread = key, a warpgroup 32 of the tile's rows
   const int wg = warp >> 2;
   const int key = threadIdx.x & 127, u = u0 + key;
-  const uint32_t tl = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + 64u * wg;
-  const float sl2 = w.scale_log2;
-  // rows (of this warpgroup's 64) whose queries see the key: tokens u .. hi - 1
+  const uint32_t tl = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + 32u * wg;
+  const uint64_t sl2 = f2(w.scale_log2, w.scale_log2);
+  // rows (of this warpgroup's 32) whose queries see the key: tokens u .. hi - 1
   const int hi = u < w.n_sink ? len : static_cast<int>(min(static_cast<long long>(len), static_cast<long long>(u) + w.window));
   for (int i = 0; i < n; ++i) {
     const int t0 = ta + i * tt;
+    // every key of the tile is seen by every row: no masks
     const bool all = t0 >= u0 + kWbKeys - 1 && t0 + tt <= len &&
                      (static_cast<long long>(t0) + tt <= static_cast<long long>(u0) + w.window || u0 + kWbKeys <= w.n_sink);
-    uint64_t mk = ~0ull;
-    if (!all)
-      mk = low_bits(static_cast<long long>(hi - t0) * w.G - 64 * wg) &
-           ~low_bits(static_cast<long long>(u - t0) * w.G - 64 * wg);
-    const float4* st = reinterpret_cast<const float4*>(S.stats[i & 1][0] + 64 * wg);
-    const float4* sd = reinterpret_cast<const float4*>(S.stats[i & 1][1] + 64 * wg);
+    const float4* st = reinterpret_cast<const float4*>(S.stats[i & 1][0] + 32 * wg);
+    const float4* sd = reinterpret_cast<const float4*>(S.stats[i & 1][1] + 32 * wg);
     mbar_wait(&S.st_full[i & 1], static_cast<uint32_t>(i >> 1) & 1u, &S.abort);
     mbar_wait(&S.s_full[0], i & 1u, &S.abort);
     tc_fence_after();
-    uint32_t v[64];  // S^T, then P^T
+    uint32_t v[32];
     tmem_ld32_nowait(tl, v);
-    tmem_ld32_nowait(tl + 32, v + 32);
+    uint64_t pr[16];  // P^T, in pairs
     tmem_wait_ld_tied(v);
-    {
-      uint32_t pk[32];
 #pragma unroll
-      for (int q = 0; q < 16; ++q) {
-        const float4 ls = st[q];
-        const float lv[4] = {ls.x, ls.y, ls.z, ls.w};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          float pr = ex2(fmaf(__uint_as_float(v[4 * q + c]), sl2, -lv[c]));
-          if (!all && !((mk >> (4 * q + c)) & 1ull)) pr = 0.f;
-          v[4 * q + c] = __float_as_uint(pr);
-        }
-        pk[2 * q] = pack_bf16(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]));
-        pk[2 * q + 1] = pack_bf16(__uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3]));
-      }
-      tmem_st32_nowait(tl, pk);
+    for (int q = 0; q < 8; ++q) {
+      const float4 ls = st[q];  // negated lse
+      pr[2 * q] = fma2(f2(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1])), sl2, f2(ls.x, ls.y));
+      pr[2 * q + 1] = fma2(f2(__uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3])), sl2, f2(ls.z, ls.w));
     }
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      float a, c;
+      unf2(pr[q], a, c);
+      pr[q] = f2(ex2(a), ex2(c));
+    }
+    uint32_t mk = 0xffffffffu;
+    if (!all) {
+      mk = static_cast<uint32_t>(low_bits(static_cast<long long>(hi - t0) * w.G - 32 * wg) &
+                                 ~low_bits(static_cast<long long>(u - t0) * w.G - 32 * wg));
+      mask_pairs(pr, mk);
+    }
+    uint32_t pk[16];
+#pragma unroll
+    for (int q = 0; q < 16; ++q) pk[q] = pack_pair(pr[q]);
+    tmem_st16_nowait(tl, pk);
     tmem_wait_st();
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&S.p_full[wg]);
+    if (lane == 0) mbar_arrive(&S.p_full);
     mbar_wait(&S.dp_full, i & 1u, &S.abort);
     tc_fence_after();
-    uint32_t pk[32];
+    tmem_ld32_nowait(tl + 128, v);
+    tmem_wait_ld_tied(v);
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      uint32_t d[32];
-      tmem_ld32_nowait(tl + 128 + 32 * hf, d);
-      tmem_wait_ld_tied(d);
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const float4 dl = sd[8 * hf + q];
-        const float lv[4] = {dl.x, dl.y, dl.z, dl.w};
-        float ds[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          ds[c] = __uint_as_float(v[32 * hf + 4 * q + c]) * (__uint_as_float(d[4 * q + c]) - lv[c]);
-          if (!all && !((mk >> (32 * hf + 4 * q + c)) & 1ull)) ds[c] = 0.f;
-        }
-        pk[16 * hf + 2 * q] = pack_bf16(ds[0], ds[1]);
-        pk[16 * hf + 2 * q + 1] = pack_bf16(ds[2], ds[3]);
-      }
+    for (int q = 0; q < 8; ++q) {
+      const float4 dl = sd[q];  // negated D
+      pr[2 * q] = mul2(pr[2 * q], add2(f2(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1])), f2(dl.x, dl.y)));
+      pr[2 * q + 1] =
+          mul2(pr[2 * q + 1], add2(f2(__uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3])), f2(dl.z, dl.w)));
     }
-    tmem_st32_nowait(tl + 128, pk);
+    if (!all) mask_pairs(pr, mk);  // dP of a masked place may be anything
+#pragma unroll
+    for (int q = 0; q < 16; ++q) pk[q] = pack_pair(pr[q]);
+    tmem_st16_nowait(tl + 128, pk);
     tmem_wait_st();
     tc_fence_before();
     __syncwarp();
     if (lane == 0) {
-      mbar_arrive(&S.ds_full[wg]);
+      mbar_arrive(&S.ds_full);
       mbar_arrive(&S.st_empty[i & 1]);
     }
   }
   mbar_wait(&S.done, 0, &S.abort);
   tc_fence_after();
-  // warpgroup 0 writes dV, warpgroup 1 dK: thread = key, its 128 values contiguous
-  const uint32_t acc = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + 256u + 128u * wg;
-  const float f = wg ? w.scale : 1.f;
+  // warpgroups 0, 1 write dV, 2, 3 dK: thread = key, half of its 128 values
+  const uint32_t acc = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + 256u + 64u * wg;
+  const int which = wg >> 1, c0 = 64 * (wg & 1);
+  const float f = which ? w.scale : 1.f;
   // slot of the partials: the CTA's place among those of split kinds
   const int slot = (sink_kind ? 0 : (p.chunks_s > 1 ? p.sink_tiles * p.chunks_s : 0)) + e2;
   const size_t item = static_cast<size_t>(slot) * (w.B * w.Hkv) + bg;
 #pragma unroll 1
-  for (int q = 0; q < 4; ++q) {
+  for (int q = 0; q < 2; ++q) {
     uint32_t v[32];
     __syncwarp();
     tmem_ld32(acc + 32 * q, v);
     if (chunks > 1) {
-      float4* dst = reinterpret_cast<float4*>(p.part + ((item * 2 + wg) * kWbKeys + key) * kHeadDim + 32 * q);
+      float4* dst = reinterpret_cast<float4*>(p.part + ((item * 2 + which) * kWbKeys + key) * kHeadDim + c0 + 32 * q);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         dst[i] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]),
                              __uint_as_float(v[4 * i + 3]));
     } else if (u < len) {
-      uint4* dst = reinterpret_cast<uint4*>((wg ? w.dk : w.dv) + (static_cast<size_t>(bg) * w.Lmax + u) * kHeadDim + 32 * q);
+      uint4* dst = reinterpret_cast<uint4*>((which ? w.dk : w.dv) + (static_cast<size_t>(bg) * w.Lmax + u) * kHeadDim + c0 + 32 * q);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         uint32_t x[4];
@@ -415,7 +438,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
     }
   }
   tc_fence_before();
-  named_bar_sync(1, 32 * 9);  // TMEM may be freed
+  named_bar_sync(1, 32 * (kWbEltWarps + 1));  // TMEM may be freed
 }
 
 // Adds the chunks of the split key tiles in order: a warp per (key, dV or dK) row.
@@ -448,22 +471,19 @@ __global__ void __launch_bounds__(256) window_dkdv_merge_kernel(const WinBwdPara
   store4((which ? w.dk : w.dv) + (static_cast<size_t>(bg) * w.Lmax + u) * kHeadDim, lane, a);
 }
 
-// grid = row_tiles * B * Hkv, the last row tiles first.  TMEM: S 0 and 128, dP 256, dQ 384.
-__global__ void __launch_bounds__(kWbThreads, 1)
-    window_dq_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
-                        const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                        const __grid_constant__ CUtensorMap tm_ks, const __grid_constant__ CUtensorMap tm_vs,
-                        const WinBwdParams p) {
-  extern __shared__ __align__(1024) unsigned char smem_1k[];
-  unsigned char* base = smem_1k;
+// One dq item: `cta` of row_tiles * B * Hkv, the last row tiles first.  TMEM: S 0 and 128,
+// dP 256, dQ 384.
+__device__ __forceinline__ void window_dq(const CUtensorMap& tm_q, const CUtensorMap& tm_do, const CUtensorMap& tm_k,
+                                          const CUtensorMap& tm_v, const CUtensorMap& tm_ks, const CUtensorMap& tm_vs,
+                                          const WinBwdParams& p, unsigned char* base, int cta) {
   unsigned char* qd = base;                        // Q tile, dO tile
   unsigned char* ring = base + 2 * kWfTileBytes;   // K / V slots: K0 V0 K1 V1 ...
   WbSmem& S = *reinterpret_cast<WbSmem*>(ring + kWbSlots * kWfTileBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const WinParams& w = p.w;
 
-  const int bg = blockIdx.x % (w.B * w.Hkv);
-  const int tile = p.row_tiles - 1 - blockIdx.x / (w.B * w.Hkv);
+  const int bg = cta % (w.B * w.Hkv);
+  const int tile = p.row_tiles - 1 - cta / (w.B * w.Hkv);
   const int b = bg / w.Hkv, g = bg - b * w.Hkv;
   const int tt = 128 >> p.g_log2;
   const int r0 = tile * tt;
@@ -481,9 +501,9 @@ __global__ void __launch_bounds__(kWbThreads, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&S.s_full[s], 1);
-      mbar_init(&S.ds_full[s], 4);
       mbar_init(&S.tail[s], 1);
     }
+    mbar_init(&S.ds_full, kWbEltWarps);
     mbar_init(&S.dp_full, 1);
     mbar_init(&S.done, 1);
     mbar_init(&S.mma_done, 1);
@@ -589,8 +609,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
       };
       bool ok = mbar_wait(&S.res_full, 0, &S.abort) && issue_s(0) && issue_dp(0) && (n < 2 || issue_s(1));
       for (int j = 0; j < n && ok; ++j) {
-        for (int h = 0; h < 2 && ok; ++h) ok = mbar_wait(&S.ds_full[h], j & 1u, &S.abort);
-        if (!ok) break;
+        if (!mbar_wait(&S.ds_full, j & 1u, &S.abort)) break;
         tc_fence_after();
         if (j + 1 < n && !issue_dp(j + 1)) break;
         umma_acc(tmem + 384, tmem + 128u * (j & 1), at(2 * j), j == 0);
@@ -601,7 +620,7 @@ __global__ void __launch_bounds__(kWbThreads, 1)
       umma_commit(&S.mma_done);
     }
     __syncwarp();
-    named_bar_sync(1, 32 * 9);
+    named_bar_sync(1, 32 * (kWbEltWarps + 1));
     if (lane == 0) mbar_wait_drain(&S.mma_done, 0);
     __syncwarp();
     tc_fence_after();
@@ -609,66 +628,60 @@ __global__ void __launch_bounds__(kWbThreads, 1)
     return;
   }
 
-  // ---------------------- elementwise: thread = row, a warpgroup one 64-key segment of the tile
+  // -------------------------- elementwise: thread = row, a warpgroup 32 keys (half a segment)
   const int wg = warp >> 2;
   const int row = threadIdx.x & 127;
   const int t = r0 + (row >> p.g_log2);
   const bool valid = t < len;
   const size_t si = ((static_cast<size_t>(bg) * p.Lp + r0) << p.g_log2) + row;
-  const float lse2 = p.lse2[si], dl = p.delta[si];
+  const float nl = p.lse2[si], nd = p.delta[si];  // negated
+  const uint64_t lse2 = f2(nl, nl), dl = f2(nd, nd), sl2 = f2(w.scale_log2, w.scale_log2);
   const uint32_t lane0 = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-  const float sl2 = w.scale_log2;
   for (int j = 0; j < n; ++j) {
-    const int seg = 2 * j + wg, u0 = runs.first_key(seg);
+    const int seg = 2 * j + (wg >> 1), u0 = runs.first_key(seg);
     const bool all = u0 + kWfSeg - 1 <= r0 && t_last == r0 + tt - 1 &&
                      (runs.is_sink(seg) ? u0 + kWfSeg <= w.n_sink
                                         : (u0 > t_last - w.window || u0 + kWfSeg <= w.n_sink));
-    const uint64_t mk = all ? ~0ull : (valid ? runs.mask(seg, t, w.window) : 0ull);
-    const uint32_t ts = tmem + lane0 + 128u * (j & 1) + 64u * wg, td = tmem + lane0 + 256u + 64u * wg;
+    const uint32_t ts = tmem + lane0 + 128u * (j & 1) + 32u * wg, td = tmem + lane0 + 256u + 32u * wg;
     mbar_wait(&S.s_full[j & 1], static_cast<uint32_t>(j >> 1) & 1u, &S.abort);
     tc_fence_after();
-    uint32_t v[64];
+    uint32_t v[32];
     tmem_ld32_nowait(ts, v);
-    tmem_ld32_nowait(ts + 32, v + 32);
+    uint64_t pr[16];
     tmem_wait_ld_tied(v);
 #pragma unroll
-    for (int c = 0; c < 64; ++c) v[c] = __float_as_uint(ex2(fmaf(__uint_as_float(v[c]), sl2, -lse2)));
+    for (int q = 0; q < 16; ++q) {
+      float a, c;
+      unf2(fma2(f2(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1])), sl2, lse2), a, c);
+      pr[q] = f2(ex2(a), ex2(c));
+    }
     mbar_wait(&S.dp_full, j & 1u, &S.abort);
     tc_fence_after();
-    uint32_t pk[32];
+    tmem_ld32_nowait(td, v);
+    tmem_wait_ld_tied(v);
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      uint32_t d[32];
-      tmem_ld32_nowait(td + 32 * hf, d);
-      tmem_wait_ld_tied(d);
+    for (int q = 0; q < 16; ++q)
+      pr[q] = mul2(pr[q], add2(f2(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1])), dl));
+    if (!all) mask_pairs(pr, valid ? static_cast<uint32_t>(runs.mask(seg, t, w.window) >> (32 * (wg & 1))) : 0u);
+    uint32_t pk[16];
 #pragma unroll
-      for (int c = 0; c < 32; c += 2) {
-        float ds[2];
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          ds[q] = __uint_as_float(v[32 * hf + c + q]) * (__uint_as_float(d[c + q]) - dl);
-          if (!all && !((mk >> (32 * hf + c + q)) & 1ull)) ds[q] = 0.f;
-        }
-        pk[16 * hf + c / 2] = pack_bf16(ds[0], ds[1]);
-      }
-    }
-    tmem_st32_nowait(ts, pk);
+    for (int q = 0; q < 16; ++q) pk[q] = pack_pair(pr[q]);
+    tmem_st16_nowait(ts, pk);
     tmem_wait_st();
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(&S.ds_full[wg]);
+    if (lane == 0) mbar_arrive(&S.ds_full);
   }
   mbar_wait(&S.done, 0, &S.abort);
   tc_fence_after();
-  // a warpgroup writes 64 of the row's 128 values
+  // a warpgroup writes 32 of the row's 128 values
   const int h = (g << p.g_log2) + (row & (w.G - 1));
-#pragma unroll 1
-  for (int q = 0; q < 2; ++q) {
+  {
     uint32_t v[32];
     __syncwarp();
-    tmem_ld32(tmem + lane0 + 384u + 64u * wg + 32 * q, v);
+    tmem_ld32(tmem + lane0 + 384u + 32u * wg, v);
     if (valid) {
-      uint4* dst = reinterpret_cast<uint4*>(w.dq + ((static_cast<size_t>(b) * w.Lq + t) * w.Hq + h) * kHeadDim + 64 * wg + 32 * q);
+      uint4* dst = reinterpret_cast<uint4*>(w.dq + ((static_cast<size_t>(b) * w.Lq + t) * w.Hq + h) * kHeadDim + 32 * wg);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         uint32_t x[4];
@@ -680,7 +693,22 @@ __global__ void __launch_bounds__(kWbThreads, 1)
     }
   }
   tc_fence_before();
-  named_bar_sync(1, 32 * 9);  // TMEM may be freed
+  named_bar_sync(1, 32 * (kWbEltWarps + 1));  // TMEM may be freed
+}
+
+// grid = the dK / dV items (long), then the dq items, which fill the SMs that the last of the
+// former leave idle.
+__global__ void __launch_bounds__(kWbThreads, 1)
+    window_bwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
+                         const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                         const __grid_constant__ CUtensorMap tm_ks, const __grid_constant__ CUtensorMap tm_vs,
+                         const WinBwdParams p) {
+  extern __shared__ __align__(1024) unsigned char smem_1k[];
+  const int cta = static_cast<int>(blockIdx.x);
+  if (cta < p.kv_items)
+    window_dkdv(tm_q, tm_do, tm_k, tm_v, p, smem_1k, cta);
+  else
+    window_dq(tm_q, tm_do, tm_k, tm_v, tm_ks, tm_vs, p, smem_1k, cta - p.kv_items);
 }
 
 }  // namespace infllmv2
