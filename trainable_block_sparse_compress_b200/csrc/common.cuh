@@ -255,6 +255,12 @@ __device__ __forceinline__ float lg2(float x) {
   return y;
 }
 
+__device__ __forceinline__ uint64_t ex2_pair(uint64_t x) {
+  float a, b;
+  unf2(x, a, b);
+  return f2(ex2(a), ex2(b));
+}
+
 __device__ __forceinline__ void named_bar_sync(int id, int nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }

@@ -120,16 +120,6 @@ __device__ __forceinline__ int window_t_end(const WinParams& w, int i, int len) 
   return static_cast<int>(min(static_cast<long long>(len), static_cast<long long>(i) * kWbKeys + kWbKeys - 1 + w.window));
 }
 
-// 16 columns of this thread's TMEM lane, without the wait (tmem_wait_st follows).
-__device__ __forceinline__ void tmem_st16_nowait(uint32_t taddr, const uint32_t (&v)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16};" ::"r"(taddr),
-      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-      : "memory");
-}
-
 // Zeroes the values of 16 pairs whose bit (0..31) is not set.
 __device__ __forceinline__ void mask_pairs(uint64_t (&v)[16], uint32_t bits) {
 #pragma unroll
@@ -363,11 +353,7 @@ __device__ __forceinline__ void window_dkdv(const CUtensorMap& tm_q, const CUten
       pr[2 * q + 1] = fma2(f2(__uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3])), sl2, f2(ls.z, ls.w));
     }
 #pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      float a, c;
-      unf2(pr[q], a, c);
-      pr[q] = f2(ex2(a), ex2(c));
-    }
+    for (int q = 0; q < 16; ++q) pr[q] = ex2_pair(pr[q]);
     uint32_t mk = 0xffffffffu;
     if (!all) {
       mk = static_cast<uint32_t>(low_bits(static_cast<long long>(hi - t0) * w.G - 32 * wg) &
@@ -650,11 +636,8 @@ __device__ __forceinline__ void window_dq(const CUtensorMap& tm_q, const CUtenso
     uint64_t pr[16];
     tmem_wait_ld_tied(v);
 #pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      float a, c;
-      unf2(fma2(f2(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1])), sl2, lse2), a, c);
-      pr[q] = f2(ex2(a), ex2(c));
-    }
+    for (int q = 0; q < 16; ++q)
+      pr[q] = ex2_pair(fma2(f2(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1])), sl2, lse2));
     mbar_wait(&S.dp_full, j & 1u, &S.abort);
     tc_fence_after();
     tmem_ld32_nowait(td, v);

@@ -30,7 +30,10 @@ constexpr int kWfTileBytes = 128 * 128 * 2;  // 32 KB: 128 rows of Q, K or V (tw
 constexpr int kWfHalf = kWfTileBytes / 2;
 constexpr int kWfSeg = 64;                   // keys of a segment
 constexpr int kWfSlots = 5;
-constexpr int kWfThreads = 32 * 10;
+constexpr int kWfThreads = 32 * 12;  // warps 10 and 11 only give their registers away
+// Registers a thread: 168 at launch (65,536 over 12 warps), then 208 for the softmax warpgroups
+// (a row's 128 scores stay in registers) and 72 for the third: 2 x 208 + 72 <= 3 x 168.
+constexpr int kWfSoftRegs = 208, kWfOtherRegs = 72;
 constexpr int kWfTmaWarp = 8, kWfMmaWarp = 9;
 constexpr uint32_t kWfColO = 256;
 
@@ -78,14 +81,13 @@ __device__ __forceinline__ void tmem_wait_ld_tied(uint32_t (&v)[N]) {
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(v[i]));
 }
 
-__device__ __forceinline__ void tmem_st32_nowait(uint32_t taddr, const uint32_t* v) {
+// 16 columns of this thread's TMEM lane, without the wait (tmem_wait_st follows).
+__device__ __forceinline__ void tmem_st16_nowait(uint32_t taddr, const uint32_t (&v)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
-      ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
-      "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]),
-      "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]),
-      "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -193,6 +195,9 @@ __global__ void __launch_bounds__(kWfThreads, 1)
   tc_fence_after();
   const uint32_t tmem = S.tmem_base;
 
+  if (warp >= kWfTmaWarp) {  // the third warpgroup, one instruction for its four warps
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWfOtherRegs));
+  if (warp > kWfMmaWarp) return;
   if (warp == kWfTmaWarp) {
     // ------------------------------------------------------------------ TMA producer
     if (lane == 0) {
@@ -262,7 +267,7 @@ __global__ void __launch_bounds__(kWfThreads, 1)
     return;
   }
 
-  if (warp == kWfMmaWarp) {
+  {
     // -------------------------------------------------------------------- MMA issuer
     if (lane == 0) {
       constexpr uint32_t id_qk = idesc_bf16_f32(128, 128, false, false), id_pv = idesc_bf16_f32(128, 128, false, true);
@@ -322,8 +327,10 @@ __global__ void __launch_bounds__(kWfThreads, 1)
     tmem_dealloc(tmem, 512);
     return;
   }
+  }
 
   // ------------------------------------------------------------------- softmax warpgroups
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWfSoftRegs));
   const int x = warp >> 2;
   const int row = threadIdx.x & 127;
   const int r = r0 + x * tt + (row >> p.g_log2);
@@ -353,12 +360,8 @@ __global__ void __launch_bounds__(kWfThreads, 1)
         if (!full) {
           const uint64_t mk = runs.mask(seg, t, w.window);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t bits = static_cast<uint32_t>(mk >> (32 * h));
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (!((bits >> i) & 1u)) v[64 * s + 32 * h + i] = 0xff800000u;  // -inf
-          }
+          for (int i = 0; i < 64; ++i)
+            if (!((mk >> i) & 1ull)) v[64 * s + i] = 0xff800000u;  // -inf
         }
       }
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -386,29 +389,30 @@ __global__ void __launch_bounds__(kWfThreads, 1)
           }
         }
       }
-      const float mr = m2 == -INFINITY ? 0.f : m2;  // nothing visible yet: every exponential is 0
-      float sm[4] = {0.f, 0.f, 0.f, 0.f};
+      const float mr = m2 == -INFINITY ? 0.f : -m2;  // nothing visible yet: every exponential is 0
+      const uint64_t sl2p = f2(sl2, sl2), mr2 = f2(mr, mr);
+      uint64_t sm[2] = {0, 0};
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t pk[32];
+      for (int h = 0; h < 4; ++h) {
+        uint32_t pk[16];
 #pragma unroll
-        for (int i = 0; i < 64; i += 4) {
-          float e[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            e[q] = ex2(fmaf(__uint_as_float(v[64 * h + i + q]), sl2, -mr));
-            sm[q] += e[q];
-          }
-          pk[i / 2] = pack_bf16(e[0], e[1]);
-          pk[i / 2 + 1] = pack_bf16(e[2], e[3]);
+        for (int i = 0; i < 16; ++i) {
+          const uint64_t e = ex2_pair(
+              fma2(f2(__uint_as_float(v[32 * h + 2 * i]), __uint_as_float(v[32 * h + 2 * i + 1])), sl2p, mr2));
+          sm[i & 1] = add2(sm[i & 1], e);
+          pk[i] = pack_pair(e);
         }
-        tmem_st32_nowait(ts + 32 * h, pk);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&S.p_full[x][h]);
+        tmem_st16_nowait(ts + 16 * h, pk);
+        if (h & 1) {
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&S.p_full[x][h >> 1]);
+        }
       }
-      sum += (sm[0] + sm[1]) + (sm[2] + sm[3]);
+      float s0, s1;
+      unf2(add2(sm[0], sm[1]), s0, s1);
+      sum += s0 + s1;
     } else {  // no row of this warp exists: its lanes of P and O are never read
       tc_fence_before();
       __syncwarp();
