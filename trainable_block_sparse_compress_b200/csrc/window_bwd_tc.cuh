@@ -32,7 +32,7 @@ constexpr int kWbSlots = 5;
 constexpr int kWbKeys = 128;  // keys of a dK / dV tile
 
 struct WbSmem {
-  uint64_t res_full, full[kWbSlots], empty[kWbSlots], s_full[2], dp_full, p_full, ds_full, done, mma_done, tail[2];
+  uint64_t res_full, full[kWbSlots], s_full[2], dp_full, p_full, ds_full, done, mma_done, tail[2];
   uint64_t st_full[2], st_empty[2];
   alignas(16) float stats[2][2][128];  // dK / dV: lse and D of a query tile's rows
   uint32_t tmem_base;
@@ -180,10 +180,7 @@ __device__ __forceinline__ void window_dkdv(const CUtensorMap& tm_q, const CUten
 
   if (threadIdx.x == 0) {
     mbar_init(&S.res_full, 1);
-    for (int s = 0; s < kWbSlots; ++s) {
-      mbar_init(&S.full[s], 1);
-      mbar_init(&S.empty[s], 1);
-    }
+    for (int s = 0; s < kWbSlots; ++s) mbar_init(&S.full[s], 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&S.s_full[s], 1);
       mbar_init(&S.tail[s], 1);
@@ -218,14 +215,20 @@ __device__ __forceinline__ void window_dkdv(const CUtensorMap& tm_q, const CUten
         }
     }
     const size_t stat0 = (static_cast<size_t>(bg) * p.Lp + ta) << p.g_log2;
-    int slot = 0;
-    uint32_t round = 0, issued = 0, stats = 0;
+    int slot = 0, issued = 0;
+    uint32_t stats = 0;
     bool tail_used = false, stop = false;
     for (int i = 0; i < n && !stop; ++i) {
       const int t0 = ta + i * tt;
       const bool any = w.q_lens != nullptr && t0 + tt > len;  // rows past the end may hold anything
       for (int kd = 0; kd < 2; ++kd) {
-        if (round > 0) mbar_wait(&S.empty[slot], (round - 1u) & 1u, &S.abort);
+        // Items 2t + 5 and 2t + 6 take the slots of Q and dO of tile t, which have been read once dP
+        // of tile t + 1 is complete (dV and dK of tile t were issued before it).  Its barrier is
+        // never two phases on: dP of tile t + 2 waits for item 2t + 5, and dP of tile 0, whose phase
+        // must be over before the next is asked for, is waited for before dP of tile 1 can start.
+        if (issued == 3) mbar_wait(&S.dp_full, 0, &S.abort);
+        if (issued >= kWbSlots && issued % 2 == 1)
+          mbar_wait(&S.dp_full, static_cast<uint32_t>((issued - kWbSlots) / 2 + 1) & 1u, &S.abort);
         if (kd == 0 && i >= 2) mbar_wait(&S.st_empty[i & 1], static_cast<uint32_t>((i >> 1) - 1) & 1u, &S.abort);
         stop = __any_sync(0xffffffffu, S.abort != 0);
         if (stop) break;
@@ -255,16 +258,13 @@ __device__ __forceinline__ void window_dkdv(const CUtensorMap& tm_q, const CUten
           if (lane == 0) mbar_arrive(&S.full[slot]);
         }
         __syncwarp();
-        if (++slot == kWbSlots) {
-          slot = 0;
-          ++round;
-        }
+        if (++slot == kWbSlots) slot = 0;
       }
     }
     if (S.abort && lane == 0) {  // let every copy this thread issued land before the CTA ends
       mbar_wait_drain(&S.res_full, 0);
-      for (uint32_t s = 0; s < kWbSlots; ++s)
-        if (issued > s) mbar_wait_drain(&S.full[s], ((issued - 1u - s) / kWbSlots) & 1u);
+      for (int s = 0; s < kWbSlots; ++s)
+        if (issued > s) mbar_wait_drain(&S.full[s], static_cast<uint32_t>((issued - 1 - s) / kWbSlots) & 1u);
       for (uint32_t s = 0; s < 2; ++s)
         if (stats > s) mbar_wait_drain(&S.st_full[s], ((stats - 1u - s) / 2) & 1u);
       if (tail_used) mbar_wait_drain(&S.tail[0], 0);
@@ -297,7 +297,6 @@ __device__ __forceinline__ void window_dkdv(const CUtensorMap& tm_q, const CUten
         if (!mbar_wait(&S.p_full, i & 1u, &S.abort)) break;
         tc_fence_after();
         umma_acc(tmem + 256, tmem, at(2 * i + 1), i == 0);
-        umma_commit(&S.empty[(2 * i + 1) % kWbSlots]);
         if (i + 1 < n) {
           if (!wait_item(2 * i + 2)) break;
           umma_rows(tmem, ka, at(2 * i + 2));
@@ -306,7 +305,6 @@ __device__ __forceinline__ void window_dkdv(const CUtensorMap& tm_q, const CUten
         if (!mbar_wait(&S.ds_full, i & 1u, &S.abort)) break;
         tc_fence_after();
         umma_acc(tmem + 384, tmem + 128, at(2 * i), i == 0);
-        umma_commit(&S.empty[(2 * i) % kWbSlots]);
         if (i + 1 < n) {
           if (!wait_item(2 * i + 3)) break;
           umma_rows(tmem + 128, va, at(2 * i + 3));
@@ -481,10 +479,7 @@ __device__ __forceinline__ void window_dq(const CUtensorMap& tm_q, const CUtenso
 
   if (threadIdx.x == 0) {
     mbar_init(&S.res_full, 1);
-    for (int s = 0; s < kWbSlots; ++s) {
-      mbar_init(&S.full[s], 1);
-      mbar_init(&S.empty[s], 1);
-    }
+    for (int s = 0; s < kWbSlots; ++s) mbar_init(&S.full[s], 1);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&S.s_full[s], 1);
       mbar_init(&S.tail[s], 1);
@@ -513,12 +508,19 @@ __device__ __forceinline__ void window_dq(const CUtensorMap& tm_q, const CUtenso
         tma_load_4d(qd + kWfTileBytes + h * kWfHalf, &tm_do, &S.res_full, 64 * h, g << p.g_log2, r0, b);
       }
     }
-    int slot = 0;
-    uint32_t round = 0, issued = 0;
+    int slot = 0, issued = 0;
     bool tail_used = false, stop = false;
     for (int j = 0; j < n && !stop; ++j)
       for (int kv = 0; kv < 2; ++kv) {
-        if (round > 0) mbar_wait(&S.empty[slot], (round - 1u) & 1u, &S.abort);
+        // Items 2t + 5 and 2t + 6 take the slots of K and V of tile t, which have been read once S of
+        // tile t + 2 is complete (dQ of tile t and dP of tile t + 1 were issued before it).  The next
+        // S on its barrier, of tile t + 4, waits for later items; S of tile 0 is waited for before S
+        // of tile 2 can start.
+        if (issued == 4) mbar_wait(&S.s_full[0], 0, &S.abort);
+        if (issued >= kWbSlots && issued % 2 == 1) {
+          const int sj = (issued - kWbSlots) / 2 + 2;
+          mbar_wait(&S.s_full[sj & 1], static_cast<uint32_t>(sj >> 1) & 1u, &S.abort);
+        }
         stop = __any_sync(0xffffffffu, S.abort != 0);
         if (stop) break;
         unsigned char* dst = ring + slot * kWfTileBytes;
@@ -555,15 +557,12 @@ __device__ __forceinline__ void window_dq(const CUtensorMap& tm_q, const CUtenso
           if (lane == 0) mbar_arrive(&S.full[slot]);
         }
         __syncwarp();
-        if (++slot == kWbSlots) {
-          slot = 0;
-          ++round;
-        }
+        if (++slot == kWbSlots) slot = 0;
       }
     if (S.abort && lane == 0) {
       mbar_wait_drain(&S.res_full, 0);
-      for (uint32_t s = 0; s < kWbSlots; ++s)
-        if (issued > s) mbar_wait_drain(&S.full[s], ((issued - 1u - s) / kWbSlots) & 1u);
+      for (int s = 0; s < kWbSlots; ++s)
+        if (issued > s) mbar_wait_drain(&S.full[s], static_cast<uint32_t>((issued - 1 - s) / kWbSlots) & 1u);
       if (tail_used) mbar_wait_drain(&S.tail[0], 0);
     }
     return;
@@ -590,7 +589,6 @@ __device__ __forceinline__ void window_dq(const CUtensorMap& tm_q, const CUtenso
         if (!wait_item(2 * j + 1)) return false;
         umma_rows(tmem + 256, da, at(2 * j + 1));
         umma_commit(&S.dp_full);
-        umma_commit(&S.empty[(2 * j + 1) % kWbSlots]);
         return true;
       };
       bool ok = mbar_wait(&S.res_full, 0, &S.abort) && issue_s(0) && issue_dp(0) && (n < 2 || issue_s(1));
@@ -599,7 +597,6 @@ __device__ __forceinline__ void window_dq(const CUtensorMap& tm_q, const CUtenso
         tc_fence_after();
         if (j + 1 < n && !issue_dp(j + 1)) break;
         umma_acc(tmem + 384, tmem + 128u * (j & 1), at(2 * j), j == 0);
-        umma_commit(&S.empty[(2 * j) % kWbSlots]);
         if (j + 2 < n && !issue_s(j + 2)) break;
       }
       umma_commit(&S.done);

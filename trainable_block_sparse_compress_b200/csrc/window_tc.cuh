@@ -14,8 +14,7 @@
 //           tile's products run under the other tile's softmax;
 //   warps 0-3 / 4-7: one softmax warpgroup per query tile, thread = row: no shuffles.  The
 //           reference maximum follows the running maximum lazily: only when a warp holds a row
-//           whose maximum rose by more than 2^8 is O rescaled (in TMEM, after the last product
-//           into it has finished); P <= 2^8 stays exact enough in bf16 and the sums are fp32.
+//           whose maximum rose by more than 2^8 is O rescaled (in TMEM); P <= 2^8 stays exact enough in bf16 and the sums are fp32.
 // P (bf16) overwrites S in TMEM: 64 of its 128 columns, written in two halves so the first
 // four K-steps of P V start before the second half's exponentials.  TMEM: S0 S1 O0 O1, all 512
 // columns.
@@ -38,7 +37,7 @@ constexpr int kWfTmaWarp = 8, kWfMmaWarp = 9;
 constexpr uint32_t kWfColO = 256;
 
 struct WfSmem {
-  uint64_t q_full[2], full[kWfSlots], empty[kWfSlots], s_full[2], p_full[2][2], o_full[2], mma_done, tail;
+  uint64_t q_full[2], full[kWfSlots], step[2], s_full[2], p_full[2][2], mma_done, tail;
   uint32_t tmem_base;
   volatile int abort;
 };
@@ -170,16 +169,13 @@ __global__ void __launch_bounds__(kWfThreads, 1)
   }
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kWfSlots; ++s) {
-      mbar_init(&S.full[s], 1);
-      mbar_init(&S.empty[s], 1);
-    }
+    for (int s = 0; s < kWfSlots; ++s) mbar_init(&S.full[s], 1);
     for (int x = 0; x < 2; ++x) {
+      mbar_init(&S.step[x], 1);
       mbar_init(&S.q_full[x], 1);
       mbar_init(&S.s_full[x], 1);
       mbar_init(&S.p_full[x][0], 4);
       mbar_init(&S.p_full[x][1], 4);
-      mbar_init(&S.o_full[x], 1);
     }
     mbar_init(&S.mma_done, 1);
     mbar_init(&S.tail, 1);
@@ -209,12 +205,17 @@ __global__ void __launch_bounds__(kWfThreads, 1)
                         b * w.Lq + r0 + x * tt);
         }
     }
-    int slot = 0;
-    uint32_t round = 0, issued = 0;
+    int slot = 0, issued = 0;
     bool tail_used = false, stop = false;
     for (int j = j0; j < j1 && !stop; ++j)
       for (int kv = 0; kv < 2; ++kv) {
-        if (round > 0) mbar_wait(&S.empty[slot], (round - 1u) & 1u, &S.abort);
+        // Step s (counted from the one before the first tile) reads items 2s - 1 and 2s, whose slots
+        // items 2s + 4 and 2s + 5 take.  Step s + 2 waits for item 2s + 4, so the barrier of step s
+        // (one of two) is never a phase further.
+        if (issued >= 4 && issued % 2 == 0) {
+          const int s = (issued - 4) / 2;
+          mbar_wait(&S.step[s & 1], static_cast<uint32_t>(s >> 1) & 1u, &S.abort);
+        }
         stop = __any_sync(0xffffffffu, S.abort != 0);
         if (stop) break;
         unsigned char* dst = ring + slot * kWfTileBytes;
@@ -252,16 +253,13 @@ __global__ void __launch_bounds__(kWfThreads, 1)
           if (lane == 0) mbar_arrive(&S.full[slot]);
         }
         __syncwarp();
-        if (++slot == kWfSlots) {
-          slot = 0;
-          ++round;
-        }
+        if (++slot == kWfSlots) slot = 0;
       }
     if (S.abort && lane == 0) {  // let every copy this thread issued land before the CTA ends
       for (int x = 0; x < 2; ++x)
         if (je[x] > jb[x]) mbar_wait_drain(&S.q_full[x], 0);
-      for (uint32_t s = 0; s < kWfSlots; ++s)
-        if (issued > s) mbar_wait_drain(&S.full[s], ((issued - 1u - s) / kWfSlots) & 1u);
+      for (int s = 0; s < kWfSlots; ++s)
+        if (issued > s) mbar_wait_drain(&S.full[s], static_cast<uint32_t>((issued - 1 - s) / kWfSlots) & 1u);
       if (tail_used) mbar_wait_drain(&S.tail, 0);
     }
     return;
@@ -308,14 +306,12 @@ __global__ void __launch_bounds__(kWfThreads, 1)
                              desc_mn_sw128(va + k * 2048, kWfHalf, 1024), id_pv, (np[x] > 0 || k > 0) ? 1u : 0u);
             }
             if (!ok) break;
-            umma_commit(&S.o_full[x]);
             ++np[x];
           }
-          if (x == 1 && j >= j0) umma_commit(&S.empty[slot_of(nv)]);
           if (j + 1 >= jb[x] && j + 1 < je[x]) issue_qk(x, slot_of(nk));
         }
         if (!ok) break;
-        if (j + 1 < j1) umma_commit(&S.empty[slot_of(nk)]);
+        umma_commit(&S.step[(j + 1 - j0) & 1]);  // V of tile j and K of tile j + 1 have been read
       }
       umma_commit(&S.mma_done);
     }
@@ -376,9 +372,7 @@ __global__ void __launch_bounds__(kWfThreads, 1)
         const float f = mn == -INFINITY ? 1.f : ex2(m2 - mn);
         m2 = mn;
         sum *= f;
-        if (n > 0) {
-          mbar_wait(&S.o_full[x], (n - 1u) & 1u, &S.abort);
-          tc_fence_after();
+        if (n > 0) {  // the last product into O came before this S: both are complete
 #pragma unroll 1
           for (int q = 0; q < 8; ++q) {
             uint32_t o16[16];
@@ -422,7 +416,7 @@ __global__ void __launch_bounds__(kWfThreads, 1)
       }
     }
   }
-  if (n > 0) mbar_wait(&S.o_full[x], (n - 1u) & 1u, &S.abort);
+  mbar_wait(&S.mma_done, 0, &S.abort);
   tc_fence_after();
   if (warp_live) {
     const int h = (g << p.g_log2) + (row & ((1 << p.g_log2) - 1));
