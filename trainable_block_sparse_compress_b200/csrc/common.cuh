@@ -105,6 +105,31 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
   }
 }
 
+// mbar_wait for waits that are short and on the critical path: the clock (whose read costs
+// hundreds of cycles) is looked at only after 64 tries.  Same limit, same return value.
+__device__ __forceinline__ bool mbar_wait_short(uint64_t* bar, uint32_t parity, volatile int* abort) {
+  const uint32_t addr = smem_u32(bar);
+  uint64_t t0 = 0;
+  for (uint32_t it = 0;; ++it) {
+    if (mbar_try_wait(addr, parity)) return true;
+    if ((it & 63u) == 63u) {
+      if (*abort) return false;
+      if ((*reinterpret_cast<volatile unsigned int*>(&g_device_error) & kDevErrWaitTimeout) != 0u) {
+        *abort = 1;
+        return false;
+      }
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0) {
+        t0 = now;
+      } else if (now - t0 > kWaitLimitNs) {
+        *abort = 1;
+        atomicOr(&g_device_error, kDevErrWaitTimeout);
+        return false;
+      }
+    }
+  }
+}
+
 // Waits like mbar_wait but ignores the CTA abort flag (only the time limit): used for
 // the final drains that must complete before TMEM or shared memory is released.
 __device__ __forceinline__ bool mbar_wait_drain(uint64_t* bar, uint32_t parity) {

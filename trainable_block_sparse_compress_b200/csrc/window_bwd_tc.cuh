@@ -130,25 +130,34 @@ __device__ __forceinline__ void mask_pairs(uint64_t (&v)[16], uint32_t bits) {
   }
 }
 
-// S or dP products: D[tmem] = A[128 rows] * B[128 rows]^T over the 128 head dimensions.
-__device__ __forceinline__ void umma_rows(uint32_t d, uint32_t a, uint32_t b) {
-  constexpr uint32_t id = idesc_bf16_f32(128, 128, false, false);
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const uint32_t o = static_cast<uint32_t>((k >> 2) * kWfHalf + (k & 3) * 32);
-    umma_bf16(d, desc_k_sw128(a + o), desc_k_sw128(b + o), id, k > 0 ? 1u : 0u);
-  }
-}
 // D[tmem] += A[tmem] * B: A holds 32 values of K in the first 16 columns of each of its four
 // 32-column quarters (a warpgroup writes its quarter over what it has read), B's 128 rows are
 // the K axis.
-__device__ __forceinline__ void umma_acc(uint32_t d, uint32_t a, uint32_t b, bool first) {
+__device__ __forceinline__ void umma_acc(uint32_t d, uint32_t a, uint64_t b, bool first) {
   constexpr uint32_t id = idesc_bf16_f32(128, 128, false, true);
 #pragma unroll
   for (int k = 0; k < 8; ++k)
-    umma_bf16_ta(d, a + 32u * (k >> 1) + 8u * (k & 1), desc_mn_sw128(b + k * 2048, kWfHalf, 1024), id,
+    umma_bf16_ta(d, a + 32u * (k >> 1) + 8u * (k & 1), b + static_cast<uint64_t>(k * (2048 >> 4)), id,
                  (!first || k > 0) ? 1u : 0u);
 }
+
+// The ring as its reader sees it: items in order, their slots counted (a division by the number
+// of slots would be on the issuing thread's path, which bounds the tensor pipe).
+struct WbRing {
+  int slot = 0;
+  uint32_t phase = 0;
+  // waits for the next item; its slot's offset in descriptor units, or -1 after a timeout
+  __device__ __forceinline__ int take(WbSmem& S) {
+    const bool ok = mbar_wait_short(&S.full[slot], phase, &S.abort);
+    tc_fence_after();
+    const int off = ok ? slot * (kWfTileBytes >> 4) : -1;
+    if (++slot == kWbSlots) {
+      slot = 0;
+      phase ^= 1u;
+    }
+    return off;
+  }
+};
 
 // One dK / dV item: `cta` of B * Hkv * (sink_tiles * chunks_s + (key_tiles - sink_tiles) *
 // chunks_w).  TMEM: S^T 0, dP^T 128, dV 256, dK 384.
@@ -226,10 +235,10 @@ __device__ __forceinline__ void window_dkdv(const CUtensorMap& tm_q, const CUten
         // of tile t + 1 is complete (dV and dK of tile t were issued before it).  Its barrier is
         // never two phases on: dP of tile t + 2 waits for item 2t + 5, and dP of tile 0, whose phase
         // must be over before the next is asked for, is waited for before dP of tile 1 can start.
-        if (issued == 3) mbar_wait(&S.dp_full, 0, &S.abort);
+        if (issued == 3) mbar_wait_short(&S.dp_full, 0, &S.abort);
         if (issued >= kWbSlots && issued % 2 == 1)
-          mbar_wait(&S.dp_full, static_cast<uint32_t>((issued - kWbSlots) / 2 + 1) & 1u, &S.abort);
-        if (kd == 0 && i >= 2) mbar_wait(&S.st_empty[i & 1], static_cast<uint32_t>((i >> 1) - 1) & 1u, &S.abort);
+          mbar_wait_short(&S.dp_full, static_cast<uint32_t>((issued - kWbSlots) / 2 + 1) & 1u, &S.abort);
+        if (kd == 0 && i >= 2) mbar_wait_short(&S.st_empty[i & 1], static_cast<uint32_t>((i >> 1) - 1) & 1u, &S.abort);
         stop = __any_sync(0xffffffffu, S.abort != 0);
         if (stop) break;
         unsigned char* dst = ring + slot * kWfTileBytes;
@@ -252,7 +261,7 @@ __device__ __forceinline__ void window_dkdv(const CUtensorMap& tm_q, const CUten
         ++issued;
         if (any) {
           tail_used = true;
-          if (mbar_wait(&S.tail[kd], 0, &S.abort)) zero_tile_rows(dst, (len - t0) << p.g_log2, lane);
+          if (mbar_wait_short(&S.tail[kd], 0, &S.abort)) zero_tile_rows(dst, (len - t0) << p.g_log2, lane);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&S.full[slot]);
@@ -274,42 +283,43 @@ __device__ __forceinline__ void window_dkdv(const CUtensorMap& tm_q, const CUten
 
   if (warp == kWbMmaWarp) {
     if (lane == 0) {
-      const uint32_t ka = smem_u32(kv), va = ka + kWfTileBytes, ra = smem_u32(ring);
-      auto at = [&](int item) { return ra + static_cast<uint32_t>(item % kWbSlots) * kWfTileBytes; };
-      auto wait_item = [&](int item) {
-        const bool ok = mbar_wait(&S.full[item % kWbSlots], static_cast<uint32_t>(item / kWbSlots) & 1u, &S.abort);
-        tc_fence_after();
-        return ok;
-      };
+      const uint64_t kd = desc_k_sw128(smem_u32(kv)), vd = kd + (kWfTileBytes >> 4);
+      const uint64_t rk = desc_k_sw128(smem_u32(ring)), rm = desc_mn_sw128(smem_u32(ring), kWfHalf, 1024);
       // Order: S(0) dP(0) | dV(i) S(i+1) | dK(i) dP(i+1).  dV(i) and S(i+1) run while dS(i) is
       // formed, dK(i) and dP(i+1) while the exponentials of tile i+1 are.
-      bool ok = mbar_wait(&S.res_full, 0, &S.abort) && wait_item(0);
+      WbRing items;
+      int q = -1, o = -1;  // offsets of tile i's Q and dO
+      bool ok = mbar_wait_short(&S.res_full, 0, &S.abort) && (q = items.take(S)) >= 0;
       if (ok) {
-        umma_rows(tmem, ka, at(0));
+        umma_rows(tmem, kd, rk + q);
         umma_commit(&S.s_full[0]);
-        ok = wait_item(1);
+        ok = (o = items.take(S)) >= 0;
       }
       if (ok) {
-        umma_rows(tmem + 128, va, at(1));
+        umma_rows(tmem + 128, vd, rk + o);
         umma_commit(&S.dp_full);
       }
       for (int i = 0; i < n && ok; ++i) {
-        if (!mbar_wait(&S.p_full, i & 1u, &S.abort)) break;
+        const bool more = i + 1 < n;
+        int qn = 0, on = 0;
+        if (!mbar_wait_short(&S.p_full, i & 1u, &S.abort)) break;
         tc_fence_after();
-        umma_acc(tmem + 256, tmem, at(2 * i + 1), i == 0);
-        if (i + 1 < n) {
-          if (!wait_item(2 * i + 2)) break;
-          umma_rows(tmem, ka, at(2 * i + 2));
+        umma_acc(tmem + 256, tmem, rm + o, i == 0);
+        if (more) {
+          if ((qn = items.take(S)) < 0) break;
+          umma_rows(tmem, kd, rk + qn);
           umma_commit(&S.s_full[0]);
         }
-        if (!mbar_wait(&S.ds_full, i & 1u, &S.abort)) break;
+        if (!mbar_wait_short(&S.ds_full, i & 1u, &S.abort)) break;
         tc_fence_after();
-        umma_acc(tmem + 384, tmem + 128, at(2 * i), i == 0);
-        if (i + 1 < n) {
-          if (!wait_item(2 * i + 3)) break;
-          umma_rows(tmem + 128, va, at(2 * i + 3));
+        umma_acc(tmem + 384, tmem + 128, rm + q, i == 0);
+        if (more) {
+          if ((on = items.take(S)) < 0) break;
+          umma_rows(tmem + 128, vd, rk + on);
           umma_commit(&S.dp_full);
         }
+        q = qn;
+        o = on;
       }
       umma_commit(&S.done);
       umma_commit(&S.mma_done);
@@ -337,8 +347,8 @@ __device__ __forceinline__ void window_dkdv(const CUtensorMap& tm_q, const CUten
                      (static_cast<long long>(t0) + tt <= static_cast<long long>(u0) + w.window || u0 + kWbKeys <= w.n_sink);
     const float4* st = reinterpret_cast<const float4*>(S.stats[i & 1][0] + 32 * wg);
     const float4* sd = reinterpret_cast<const float4*>(S.stats[i & 1][1] + 32 * wg);
-    mbar_wait(&S.st_full[i & 1], static_cast<uint32_t>(i >> 1) & 1u, &S.abort);
-    mbar_wait(&S.s_full[0], i & 1u, &S.abort);
+    mbar_wait_short(&S.st_full[i & 1], static_cast<uint32_t>(i >> 1) & 1u, &S.abort);
+    mbar_wait_short(&S.s_full[0], i & 1u, &S.abort);
     tc_fence_after();
     uint32_t v[32];
     tmem_ld32_nowait(tl, v);
@@ -366,7 +376,7 @@ __device__ __forceinline__ void window_dkdv(const CUtensorMap& tm_q, const CUten
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(&S.p_full);
-    mbar_wait(&S.dp_full, i & 1u, &S.abort);
+    mbar_wait_short(&S.dp_full, i & 1u, &S.abort);
     tc_fence_after();
     tmem_ld32_nowait(tl + 128, v);
     tmem_wait_ld_tied(v);
@@ -389,7 +399,7 @@ __device__ __forceinline__ void window_dkdv(const CUtensorMap& tm_q, const CUten
       mbar_arrive(&S.st_empty[i & 1]);
     }
   }
-  mbar_wait(&S.done, 0, &S.abort);
+  mbar_wait_short(&S.done, 0, &S.abort);
   tc_fence_after();
   // warpgroups 0, 1 write dV, 2, 3 dK: thread = key, half of its 128 values
   const uint32_t acc = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + 256u + 64u * wg;
@@ -516,10 +526,10 @@ __device__ __forceinline__ void window_dq(const CUtensorMap& tm_q, const CUtenso
         // tile t + 2 is complete (dQ of tile t and dP of tile t + 1 were issued before it).  The next
         // S on its barrier, of tile t + 4, waits for later items; S of tile 0 is waited for before S
         // of tile 2 can start.
-        if (issued == 4) mbar_wait(&S.s_full[0], 0, &S.abort);
+        if (issued == 4) mbar_wait_short(&S.s_full[0], 0, &S.abort);
         if (issued >= kWbSlots && issued % 2 == 1) {
           const int sj = (issued - kWbSlots) / 2 + 2;
-          mbar_wait(&S.s_full[sj & 1], static_cast<uint32_t>(sj >> 1) & 1u, &S.abort);
+          mbar_wait_short(&S.s_full[sj & 1], static_cast<uint32_t>(sj >> 1) & 1u, &S.abort);
         }
         stop = __any_sync(0xffffffffu, S.abort != 0);
         if (stop) break;
@@ -547,7 +557,7 @@ __device__ __forceinline__ void window_dq(const CUtensorMap& tm_q, const CUtenso
         ++issued;
         if (any) {
           tail_used = true;
-          if (mbar_wait(&S.tail[0], 0, &S.abort))
+          if (mbar_wait_short(&S.tail[0], 0, &S.abort))
             for (int s = 0; s < 2; ++s)
               for (int i = max(clean[s], 0) * 8 + lane; i < kWfSeg * 8; i += 32)
                 for (int h = 0; h < 2; ++h)
@@ -570,34 +580,33 @@ __device__ __forceinline__ void window_dq(const CUtensorMap& tm_q, const CUtenso
 
   if (warp == kWbMmaWarp) {
     if (lane == 0) {
-      const uint32_t qa = smem_u32(qd), da = qa + kWfTileBytes, ra = smem_u32(ring);
-      auto at = [&](int item) { return ra + static_cast<uint32_t>(item % kWbSlots) * kWfTileBytes; };
-      auto wait_item = [&](int item) {
-        const bool ok = mbar_wait(&S.full[item % kWbSlots], static_cast<uint32_t>(item / kWbSlots) & 1u, &S.abort);
-        tc_fence_after();
-        return ok;
-      };
+      const uint64_t qdesc = desc_k_sw128(smem_u32(qd)), ddesc = qdesc + (kWfTileBytes >> 4);
+      const uint64_t rk = desc_k_sw128(smem_u32(ring)), rm = desc_mn_sw128(smem_u32(ring), kWfHalf, 1024);
       // Order: S(0) dP(0) S(1) | dP(j+1) dQ(j) S(j+2): the next tile's scores and dP are there when
       // its exponentials start.
-      auto issue_s = [&](int j) {
-        if (!wait_item(2 * j)) return false;
-        umma_rows(tmem + 128u * (j & 1), qa, at(2 * j));
+      WbRing items;
+      int k0 = -1, k1 = -1;  // offsets of K of tiles j and j + 1
+      auto issue_s = [&](int j, int& k) {
+        if ((k = items.take(S)) < 0) return false;
+        umma_rows(tmem + 128u * (j & 1), qdesc, rk + k);
         umma_commit(&S.s_full[j & 1]);
         return true;
       };
-      auto issue_dp = [&](int j) {
-        if (!wait_item(2 * j + 1)) return false;
-        umma_rows(tmem + 256, da, at(2 * j + 1));
+      auto issue_dp = [&] {
+        const int v = items.take(S);
+        if (v < 0) return false;
+        umma_rows(tmem + 256, ddesc, rk + v);
         umma_commit(&S.dp_full);
         return true;
       };
-      bool ok = mbar_wait(&S.res_full, 0, &S.abort) && issue_s(0) && issue_dp(0) && (n < 2 || issue_s(1));
+      bool ok = mbar_wait_short(&S.res_full, 0, &S.abort) && issue_s(0, k0) && issue_dp() && (n < 2 || issue_s(1, k1));
       for (int j = 0; j < n && ok; ++j) {
-        if (!mbar_wait(&S.ds_full, j & 1u, &S.abort)) break;
+        if (!mbar_wait_short(&S.ds_full, j & 1u, &S.abort)) break;
         tc_fence_after();
-        if (j + 1 < n && !issue_dp(j + 1)) break;
-        umma_acc(tmem + 384, tmem + 128u * (j & 1), at(2 * j), j == 0);
-        if (j + 2 < n && !issue_s(j + 2)) break;
+        if (j + 1 < n && !issue_dp()) break;
+        umma_acc(tmem + 384, tmem + 128u * (j & 1), rm + k0, j == 0);
+        k0 = k1;
+        if (j + 2 < n && !issue_s(j + 2, k1)) break;
       }
       umma_commit(&S.done);
       umma_commit(&S.mma_done);
@@ -626,7 +635,7 @@ __device__ __forceinline__ void window_dq(const CUtensorMap& tm_q, const CUtenso
                      (runs.is_sink(seg) ? u0 + kWfSeg <= w.n_sink
                                         : (u0 > t_last - w.window || u0 + kWfSeg <= w.n_sink));
     const uint32_t ts = tmem + lane0 + 128u * (j & 1) + 32u * wg, td = tmem + lane0 + 256u + 32u * wg;
-    mbar_wait(&S.s_full[j & 1], static_cast<uint32_t>(j >> 1) & 1u, &S.abort);
+    mbar_wait_short(&S.s_full[j & 1], static_cast<uint32_t>(j >> 1) & 1u, &S.abort);
     tc_fence_after();
     uint32_t v[32];
     tmem_ld32_nowait(ts, v);
@@ -635,7 +644,7 @@ __device__ __forceinline__ void window_dq(const CUtensorMap& tm_q, const CUtenso
 #pragma unroll
     for (int q = 0; q < 16; ++q)
       pr[q] = ex2_pair(fma2(f2(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1])), sl2, lse2));
-    mbar_wait(&S.dp_full, j & 1u, &S.abort);
+    mbar_wait_short(&S.dp_full, j & 1u, &S.abort);
     tc_fence_after();
     tmem_ld32_nowait(td, v);
     tmem_wait_ld_tied(v);
@@ -652,7 +661,7 @@ __device__ __forceinline__ void window_dq(const CUtensorMap& tm_q, const CUtenso
     __syncwarp();
     if (lane == 0) mbar_arrive(&S.ds_full);
   }
-  mbar_wait(&S.done, 0, &S.abort);
+  mbar_wait_short(&S.done, 0, &S.abort);
   tc_fence_after();
   // a warpgroup writes 32 of the row's 128 values
   const int h = (g << p.g_log2) + (row & (w.G - 1));

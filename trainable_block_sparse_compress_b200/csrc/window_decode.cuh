@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kWdThreads, 2)
     if (lane == 0) {
       for (int i = 0; i < n; ++i) {
         const int st = i % kWdStages, seg = s0 + i;
-        if (i >= kWdStages) mbar_wait(&S.empty[st], static_cast<uint32_t>(i / kWdStages - 1) & 1u, &S.abort);
+        if (i >= kWdStages) mbar_wait_short(&S.empty[st], static_cast<uint32_t>(i / kWdStages - 1) & 1u, &S.abort);
         if (S.abort) {  // let every copy this thread issued land before the CTA ends
           for (int s = 0; s < kWdStages; ++s)
             if (i > s) mbar_wait_drain(&S.full[s], static_cast<uint32_t>((i - 1 - s) / kWdStages) & 1u);
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kWdThreads, 2)
     const int key_w = 16 * warp;  // this warp's keys of a segment
     for (int i = 0; i < n; ++i) {
       const int st = i % kWdStages, seg = s0 + i;
-      mbar_wait(&S.full[st], static_cast<uint32_t>(i / kWdStages) & 1u, &S.abort);
+      mbar_wait_short(&S.full[st], static_cast<uint32_t>(i / kWdStages) & 1u, &S.abort);
       unsigned char* kt = ring + st * kWdStageBytes;
       unsigned char* vt = kt + 2 * kWdHalf;
       // keys of this warp that the query sees: a prefix of the segment's, in either run

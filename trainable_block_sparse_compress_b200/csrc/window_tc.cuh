@@ -58,6 +58,24 @@ __device__ __forceinline__ void umma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, u
       : "memory");
 }
 
+// Products over 128 head dimensions: D[tmem] = A[128 rows] * B[128 rows]^T, both tiles K-major
+// (descriptors of their first bytes).
+__device__ __forceinline__ void umma_rows(uint32_t d, uint64_t a, uint64_t b) {
+  constexpr uint32_t id = idesc_bf16_f32(128, 128, false, false);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint64_t o = static_cast<uint64_t>(((k >> 2) * kWfHalf + (k & 3) * 32) >> 4);
+    umma_bf16(d, a + o, b + o, id, k > 0 ? 1u : 0u);
+  }
+}
+// D[tmem] (+)= A[tmem] * B: 64 values of K, A in 32 columns, B's 64 rows (of 128 values).
+__device__ __forceinline__ void umma_pv_half(uint32_t d, uint32_t a, uint64_t b, bool accumulate) {
+  constexpr uint32_t id = idesc_bf16_f32(128, 128, false, true);
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    umma_bf16_ta(d, a + 8u * k, b + static_cast<uint64_t>(k * (2048 >> 4)), id, (accumulate || k > 0) ? 1u : 0u);
+}
+
 // 32 columns of this thread's TMEM lane into v[0..31], without the wait (tmem_wait_ld follows).
 __device__ __forceinline__ void tmem_ld32_nowait(uint32_t taddr, uint32_t* v) {
   asm volatile(
@@ -214,7 +232,7 @@ __global__ void __launch_bounds__(kWfThreads, 1)
         // (one of two) is never a phase further.
         if (issued >= 4 && issued % 2 == 0) {
           const int s = (issued - 4) / 2;
-          mbar_wait(&S.step[s & 1], static_cast<uint32_t>(s >> 1) & 1u, &S.abort);
+          mbar_wait_short(&S.step[s & 1], static_cast<uint32_t>(s >> 1) & 1u, &S.abort);
         }
         stop = __any_sync(0xffffffffu, S.abort != 0);
         if (stop) break;
@@ -243,7 +261,7 @@ __global__ void __launch_bounds__(kWfThreads, 1)
         ++issued;
         if (any) {
           tail_used = true;
-          if (mbar_wait(&S.tail, 0, &S.abort))
+          if (mbar_wait_short(&S.tail, 0, &S.abort))
             for (int s = 0; s < 2; ++s)
               for (int i = max(clean[s], 0) * 8 + lane; i < kWfSeg * 8; i += 32)
                 for (int h = 0; h < 2; ++h)
@@ -267,54 +285,76 @@ __global__ void __launch_bounds__(kWfThreads, 1)
 
   {
     // -------------------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t id_qk = idesc_bf16_f32(128, 128, false, false), id_pv = idesc_bf16_f32(128, 128, false, true);
-      const uint32_t q0 = smem_u32(qs), r0a = smem_u32(ring);
-      uint32_t np[2] = {0, 0};  // probability tiles consumed per query tile
-      auto issue_qk = [&](int x, int slot) {
-        const uint32_t qa = q0 + x * kWfTileBytes, ka = r0a + slot * kWfTileBytes;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t o = static_cast<uint32_t>((k >> 2) * kWfHalf + (k & 3) * 32);
-          umma_bf16(tmem + 128u * x, desc_k_sw128(qa + o), desc_k_sw128(ka + o), id_qk, k > 0 ? 1u : 0u);
-        }
-        umma_commit(&S.s_full[x]);
-      };
-      // item n of the ring: K of tile j is n = 2 (j - j0), V is n + 1
-      auto slot_of = [](int n) { return n % kWfSlots; };
-      auto wait_item = [&](int n) {
-        const bool ok = mbar_wait(&S.full[slot_of(n)], static_cast<uint32_t>(n / kWfSlots) & 1u, &S.abort);
-        tc_fence_after();
-        return ok;
-      };
-      for (int x = 0; x < 2; ++x)
-        if (je[x] > jb[x]) mbar_wait(&S.q_full[x], 0, &S.abort);
-      for (int j = j0 - 1; j < j1; ++j) {
-        const int nv = 2 * (j - j0) + 1, nk = nv + 1;
-        if (j >= j0 && !wait_item(nv)) break;
-        if (j + 1 < j1 && !wait_item(nk)) break;
-        bool ok = true;
-        for (int x = 0; x < 2; ++x) {
-          if (j >= jb[x] && j < je[x]) {
-            const uint32_t va = r0a + slot_of(nv) * kWfTileBytes;
-            for (int h = 0; h < 2 && ok; ++h) {
-              ok = mbar_wait(&S.p_full[x][h], np[x] & 1u, &S.abort);
-              tc_fence_after();
-#pragma unroll
-              for (int k = 4 * h; k < 4 * h + 4; ++k)
-                umma_bf16_ta(tmem + kWfColO + 128u * x, tmem + 128u * x + 8u * k,
-                             desc_mn_sw128(va + k * 2048, kWfHalf, 1024), id_pv, (np[x] > 0 || k > 0) ? 1u : 0u);
-            }
-            if (!ok) break;
-            ++np[x];
-          }
-          if (j + 1 >= jb[x] && j + 1 < je[x]) issue_qk(x, slot_of(nk));
-        }
-        if (!ok) break;
-        umma_commit(&S.step[(j + 1 - j0) & 1]);  // V of tile j and K of tile j + 1 have been read
+    // The tensor pipe holds about four products (256 cycles) beyond the one it runs, a completed
+    // barrier takes this warp ~120 cycles to see, and a wait for an operand that is there already
+    // must not let the pipe run empty: each barrier is probed (without blocking) before the batch
+    // of products that precedes its use.
+    const bool lead = elect_one();
+    const uint64_t qd = desc_k_sw128(smem_u32(qs)), kd = desc_k_sw128(smem_u32(ring));
+    const uint64_t vd = desc_mn_sw128(smem_u32(ring), kWfHalf, 1024);
+    bool ok = true;
+    auto need = [&](bool seen, uint64_t* bar, uint32_t parity) {
+      if (ok && !seen) ok = mbar_wait_short(bar, parity, &S.abort);
+    };
+    for (int x = 0; x < 2; ++x)
+      if (je[x] > jb[x]) need(false, &S.q_full[x], 0);
+    uint32_t np0 = 0, np1 = 0;  // probability tiles consumed per query tile
+    int slot = 0;               // ring position of the next item (K of a tile, then its V)
+    uint32_t phase = 0;
+    auto advance = [&] {
+      if (++slot == kWfSlots) {
+        slot = 0;
+        phase ^= 1u;
       }
-      umma_commit(&S.mma_done);
+    };
+    // O_x += P_x V and S_x = Q_x K of the next tile.  `then` probes a barrier needed after it.
+    auto run_tile = [&](int x, uint32_t& np, bool pv, bool qk, bool p_seen, uint64_t v, uint64_t k, uint64_t* kbar,
+                        uint32_t kphase, bool k_known) {
+      bool k_seen = k_known;
+      if (pv) {
+        need(p_seen, &S.p_full[x][0], np & 1u);
+        const bool h1 = mbar_test(&S.p_full[x][1], np & 1u);
+        tc_fence_after();
+        if (ok && lead) umma_pv_half(tmem + kWfColO + 128u * x, tmem + 128u * x, v, np > 0);
+        need(h1, &S.p_full[x][1], np & 1u);
+        if (qk && !k_known) k_seen = mbar_test(kbar, kphase);
+        tc_fence_after();
+        if (ok && lead) umma_pv_half(tmem + kWfColO + 128u * x, tmem + 128u * x + 32u, v + 512u, true);
+        ++np;
+      }
+      if (qk) {
+        need(k_seen, kbar, kphase);
+        if (ok && lead) {
+          umma_rows(tmem + 128u * x, qd + x * (kWfTileBytes >> 4), k);
+          umma_commit(&S.s_full[x]);
+        }
+      }
+    };
+    for (int j = j0 - 1; j < j1 && ok; ++j) {
+      const bool pv0 = j >= jb[0] && j < je[0], qk0 = j + 1 >= jb[0] && j + 1 < je[0];
+      const bool pv1 = j >= jb[1] && j < je[1], qk1 = j + 1 >= jb[1] && j + 1 < je[1];
+      const bool p0 = pv0 && mbar_test(&S.p_full[0][0], np0 & 1u);
+      uint64_t v = vd, k = kd;
+      if (j >= j0) {
+        need(false, &S.full[slot], phase);  // V came with the K read a step ago: seen at once
+        v += static_cast<uint32_t>(slot) * (kWfTileBytes >> 4);
+        advance();
+      }
+      uint64_t* const kbar = &S.full[slot];
+      const uint32_t kphase = phase;
+      const bool has_k = j + 1 < j1;
+      if (has_k) {
+        k += static_cast<uint32_t>(slot) * (kWfTileBytes >> 4);
+        advance();
+      }
+      run_tile(0, np0, pv0, qk0, p0, v, k, kbar, kphase, false);
+      const bool p1 = pv1 && mbar_test(&S.p_full[1][0], np1 & 1u);
+      run_tile(1, np1, pv1, qk1, p1, v, k, kbar, kphase, qk0);
+      if (ok && has_k && !qk0 && !qk1) need(false, kbar, kphase);  // its slot is released below all the same
+      if (ok && lead) umma_commit(&S.step[(j + 1 - j0) & 1]);  // V of tile j and K of tile j + 1 have been read
+      __syncwarp();
     }
+    if (lead) umma_commit(&S.mma_done);
     __syncwarp();
     named_bar_sync(1, 32 * 9);  // the softmax warps have used TMEM for the last time
     if (lane == 0) mbar_wait_drain(&S.mma_done, 0);
@@ -340,7 +380,7 @@ __global__ void __launch_bounds__(kWfThreads, 1)
   float m2 = -INFINITY, sum = 0.f;  // reference maximum (scaled, base 2) and sum of the row
   uint32_t n = 0;
   for (int j = jb[x]; j < je[x]; ++j, ++n) {
-    mbar_wait(&S.s_full[x], n & 1u, &S.abort);  // after a timeout the loop runs on: its loads are collective
+    mbar_wait_short(&S.s_full[x], n & 1u, &S.abort);  // after a timeout the loop runs on: its loads are collective
     tc_fence_after();
     if (warp_live) {
       uint32_t v[128];
@@ -416,7 +456,7 @@ __global__ void __launch_bounds__(kWfThreads, 1)
       }
     }
   }
-  mbar_wait(&S.mma_done, 0, &S.abort);
+  mbar_wait_short(&S.mma_done, 0, &S.abort);
   tc_fence_after();
   if (warp_live) {
     const int h = (g << p.g_log2) + (row & ((1 << p.g_log2) - 1));
