@@ -400,22 +400,27 @@ def qk_norm_rope(p: Params, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, t
             _need(t, name, torch.int32, (p.batch,))
     if (k_cache is None) != (v_cache is None):
         raise ValueError("k_cache and v_cache go together")
+    # outputs made here need no checks
     if q_out is None:
         q_out = q.new_empty((B, Lq, p.num_q_heads, p.head_dim))
-    _need(q_out, "q_out", torch.bfloat16, (B, Lq, p.num_q_heads, p.head_dim))
+    else:
+        _need(q_out, "q_out", torch.bfloat16, (B, Lq, p.num_q_heads, p.head_dim))
     if k_cache is not None:
         if k_out is not None or v_out is not None:
             raise ValueError("k_out and v_out are for fresh outputs, without caches")
-        k_out, v_out, Lout = k_cache, v_cache, k_cache.shape[2]
+        Lout = k_cache.shape[2]
+        for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+            _need(t, name, torch.bfloat16, (B, p.num_kv_heads, Lout, p.head_dim))
+        k_out, v_out = k_cache, v_cache
     else:
         Lout = Lq
+        for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+            if t is not None:
+                _need(t, name, torch.bfloat16, (B, p.num_kv_heads, Lq, p.head_dim))
         if k_out is None:
             k_out = q.new_empty((B, p.num_kv_heads, Lq, p.head_dim))
         if v_out is None:
             v_out = torch.empty_like(k_out)
-    for t, name in ((k_out, "k_cache" if k_cache is not None else "k_out"),
-                    (v_out, "v_cache" if k_cache is not None else "v_out")):
-        _need(t, name, torch.bfloat16, (B, p.num_kv_heads, Lout, p.head_dim))
     st = _lib.load().infllmv2_qk_norm_rope(ctypes.byref(p.c()), _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, Lq,
                                            _ptr(q_weight), _ptr(k_weight), wf, eps, _ptr(table), n, rot,
                                            int(interleaved), _ptr(starts), _ptr(q_lens), _ptr(q_out), _ptr(k_out),
@@ -483,11 +488,12 @@ def window_attn_chunk(p: Params, q: torch.Tensor, k: torch.Tensor, v: torch.Tens
             _need(t, name, torch.int32, (p.batch,))
     if out is None:
         out = torch.empty_like(q)
-    _need(out, "o", torch.bfloat16, tuple(q.shape))
-    if want_lse and lse is None:
-        lse = torch.empty((B, Hq, Lq), dtype=torch.float32, device=q.device)
+    else:
+        _need(out, "o", torch.bfloat16, q.shape)
     if lse is not None:
         _need(lse, "lse", torch.float32, (B, Hq, Lq))
+    elif want_lse:
+        lse = q.new_empty((B, Hq, Lq), dtype=torch.float32)
     ws = _workspace(p, _lib.OP_WINDOW_ATTN, Lq, ws, q.device)
     nbytes = 0 if ws is None else ws.numel() * ws.element_size()
     st = _lib.load().infllmv2_window_attn(ctypes.byref(p.c()), _ptr(q), Lq, _ptr(k), _ptr(v), _ptr(q_lens),
@@ -523,11 +529,12 @@ def window_attn_decode(p: Params, q: torch.Tensor, k_cache: torch.Tensor, v_cach
     _need(lens, "lens", torch.int32, (p.batch,))
     if out is None:
         out = torch.empty_like(q)
-    _need(out, "o", torch.bfloat16, tuple(q.shape))
-    if want_lse and lse is None:
-        lse = torch.empty((p.batch, p.num_q_heads), dtype=torch.float32, device=q.device)
+    else:
+        _need(out, "o", torch.bfloat16, q.shape)
     if lse is not None:
         _need(lse, "lse", torch.float32, (p.batch, p.num_q_heads))
+    elif want_lse:
+        lse = q.new_empty((p.batch, p.num_q_heads), dtype=torch.float32)
     ws = _workspace(p, _lib.OP_WINDOW_DECODE, Lmax, ws, q.device)
     nbytes = 0 if ws is None else ws.numel() * ws.element_size()
     st = _lib.load().infllmv2_window_attn_decode(ctypes.byref(p.c()), _ptr(q), _ptr(k_cache), _ptr(v_cache),
@@ -553,11 +560,12 @@ def window_attn_backward(p: Params, q: torch.Tensor, k: torch.Tensor, v: torch.T
     _need(lse, "lse", torch.float32, (p.batch, p.num_q_heads, L))
     if lens is not None:
         _need(lens, "lens", torch.int32, (p.batch,))
+    for t, ref, name in ((dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv")):
+        if t is not None:
+            _need(t, name, torch.bfloat16, ref.shape)
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
-    for t, ref, name in ((dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv")):
-        _need(t, name, torch.bfloat16, tuple(ref.shape))
     ws = _workspace(p, _lib.OP_WINDOW_BACKWARD, L, ws, q.device)
     nbytes = 0 if ws is None else ws.numel() * ws.element_size()
     st = _lib.load().infllmv2_window_attn_backward(ctypes.byref(p.c()), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse),
