@@ -282,45 +282,54 @@ __device__ __forceinline__ void window_dkdv(const CUtensorMap& tm_q, const CUten
   }
 
   if (warp == kWbMmaWarp) {
-    if (lane == 0) {
-      const uint64_t kd = desc_k_sw128(smem_u32(kv)), vd = kd + (kWfTileBytes >> 4);
-      const uint64_t rk = desc_k_sw128(smem_u32(ring)), rm = desc_mn_sw128(smem_u32(ring), kWfHalf, 1024);
-      // Order: S(0) dP(0) | dV(i) S(i+1) | dK(i) dP(i+1).  dV(i) and S(i+1) run while dS(i) is
-      // formed, dK(i) and dP(i+1) while the exponentials of tile i+1 are.
-      WbRing items;
-      int q = -1, o = -1;  // offsets of tile i's Q and dO
-      bool ok = mbar_wait_short(&S.res_full, 0, &S.abort) && (q = items.take(S)) >= 0;
-      if (ok) {
+    // The warp stays converged: with the operands in uniform registers a product takes few issue
+    // slots, for which this warp competes with the elementwise warps of its scheduler.
+    const bool lead = elect_one();
+    const uint64_t kd = desc_k_sw128(smem_u32(kv)), vd = kd + (kWfTileBytes >> 4);
+    const uint64_t rk = desc_k_sw128(smem_u32(ring)), rm = desc_mn_sw128(smem_u32(ring), kWfHalf, 1024);
+    // Order: S(0) dP(0) | dV(i) S(i+1) | dK(i) dP(i+1).  dV(i) and S(i+1) run while dS(i) is
+    // formed, dK(i) and dP(i+1) while the exponentials of tile i+1 are.
+    WbRing items;
+    int q = -1, o = -1;  // offsets of tile i's Q and dO
+    bool ok = mbar_wait_short(&S.res_full, 0, &S.abort) && (q = items.take(S)) >= 0;
+    if (ok) {
+      if (lead) {
         umma_rows(tmem, kd, rk + q);
         umma_commit(&S.s_full[0]);
-        ok = (o = items.take(S)) >= 0;
       }
-      if (ok) {
-        umma_rows(tmem + 128, vd, rk + o);
-        umma_commit(&S.dp_full);
-      }
-      for (int i = 0; i < n && ok; ++i) {
-        const bool more = i + 1 < n;
-        int qn = 0, on = 0;
-        if (!mbar_wait_short(&S.p_full, i & 1u, &S.abort)) break;
-        tc_fence_after();
-        umma_acc(tmem + 256, tmem, rm + o, i == 0);
-        if (more) {
-          if ((qn = items.take(S)) < 0) break;
+      ok = (o = items.take(S)) >= 0;
+    }
+    if (ok && lead) {
+      umma_rows(tmem + 128, vd, rk + o);
+      umma_commit(&S.dp_full);
+    }
+    for (int i = 0; i < n && ok; ++i) {
+      const bool more = i + 1 < n;
+      int qn = 0, on = 0;
+      if (!mbar_wait_short(&S.p_full, i & 1u, &S.abort)) break;
+      tc_fence_after();
+      if (lead) umma_acc(tmem + 256, tmem, rm + o, i == 0);
+      if (more) {
+        if ((qn = items.take(S)) < 0) break;
+        if (lead) {
           umma_rows(tmem, kd, rk + qn);
           umma_commit(&S.s_full[0]);
         }
-        if (!mbar_wait_short(&S.ds_full, i & 1u, &S.abort)) break;
-        tc_fence_after();
-        umma_acc(tmem + 384, tmem + 128, rm + q, i == 0);
-        if (more) {
-          if ((on = items.take(S)) < 0) break;
+      }
+      if (!mbar_wait_short(&S.ds_full, i & 1u, &S.abort)) break;
+      tc_fence_after();
+      if (lead) umma_acc(tmem + 384, tmem + 128, rm + q, i == 0);
+      if (more) {
+        if ((on = items.take(S)) < 0) break;
+        if (lead) {
           umma_rows(tmem + 128, vd, rk + on);
           umma_commit(&S.dp_full);
         }
-        q = qn;
-        o = on;
       }
+      q = qn;
+      o = on;
+    }
+    if (lead) {
       umma_commit(&S.done);
       umma_commit(&S.mma_done);
     }
@@ -579,35 +588,40 @@ __device__ __forceinline__ void window_dq(const CUtensorMap& tm_q, const CUtenso
   }
 
   if (warp == kWbMmaWarp) {
-    if (lane == 0) {
-      const uint64_t qdesc = desc_k_sw128(smem_u32(qd)), ddesc = qdesc + (kWfTileBytes >> 4);
-      const uint64_t rk = desc_k_sw128(smem_u32(ring)), rm = desc_mn_sw128(smem_u32(ring), kWfHalf, 1024);
-      // Order: S(0) dP(0) S(1) | dP(j+1) dQ(j) S(j+2): the next tile's scores and dP are there when
-      // its exponentials start.
-      WbRing items;
-      int k0 = -1, k1 = -1;  // offsets of K of tiles j and j + 1
-      auto issue_s = [&](int j, int& k) {
-        if ((k = items.take(S)) < 0) return false;
+    const bool lead = elect_one();  // as for dK / dV
+    const uint64_t qdesc = desc_k_sw128(smem_u32(qd)), ddesc = qdesc + (kWfTileBytes >> 4);
+    const uint64_t rk = desc_k_sw128(smem_u32(ring)), rm = desc_mn_sw128(smem_u32(ring), kWfHalf, 1024);
+    // Order: S(0) dP(0) S(1) | dP(j+1) dQ(j) S(j+2): the next tile's scores and dP are there when
+    // its exponentials start.
+    WbRing items;
+    int k0 = -1, k1 = -1;  // offsets of K of tiles j and j + 1
+    auto issue_s = [&](int j, int& k) {
+      if ((k = items.take(S)) < 0) return false;
+      if (lead) {
         umma_rows(tmem + 128u * (j & 1), qdesc, rk + k);
         umma_commit(&S.s_full[j & 1]);
-        return true;
-      };
-      auto issue_dp = [&] {
-        const int v = items.take(S);
-        if (v < 0) return false;
+      }
+      return true;
+    };
+    auto issue_dp = [&] {
+      const int v = items.take(S);
+      if (v < 0) return false;
+      if (lead) {
         umma_rows(tmem + 256, ddesc, rk + v);
         umma_commit(&S.dp_full);
-        return true;
-      };
-      bool ok = mbar_wait_short(&S.res_full, 0, &S.abort) && issue_s(0, k0) && issue_dp() && (n < 2 || issue_s(1, k1));
-      for (int j = 0; j < n && ok; ++j) {
-        if (!mbar_wait_short(&S.ds_full, j & 1u, &S.abort)) break;
-        tc_fence_after();
-        if (j + 1 < n && !issue_dp()) break;
-        umma_acc(tmem + 384, tmem + 128u * (j & 1), rm + k0, j == 0);
-        k0 = k1;
-        if (j + 2 < n && !issue_s(j + 2, k1)) break;
       }
+      return true;
+    };
+    bool ok = mbar_wait_short(&S.res_full, 0, &S.abort) && issue_s(0, k0) && issue_dp() && (n < 2 || issue_s(1, k1));
+    for (int j = 0; j < n && ok; ++j) {
+      if (!mbar_wait_short(&S.ds_full, j & 1u, &S.abort)) break;
+      tc_fence_after();
+      if (j + 1 < n && !issue_dp()) break;
+      if (lead) umma_acc(tmem + 384, tmem + 128u * (j & 1), rm + k0, j == 0);
+      k0 = k1;
+      if (j + 2 < n && !issue_s(j + 2, k1)) break;
+    }
+    if (lead) {
       umma_commit(&S.done);
       umma_commit(&S.mma_done);
     }
