@@ -146,9 +146,12 @@ __device__ __forceinline__ void umma_acc(uint32_t d, uint32_t a, uint64_t b, boo
 struct WbRing {
   int slot = 0;
   uint32_t phase = 0;
+  // has the next item landed?  Asked a batch of products ahead of take(), which costs ~120 cycles
+  // when it has to look.
+  __device__ __forceinline__ bool probe(WbSmem& S) const { return mbar_test(&S.full[slot], phase); }
   // waits for the next item; its slot's offset in descriptor units, or -1 after a timeout
-  __device__ __forceinline__ int take(WbSmem& S) {
-    const bool ok = mbar_wait_short(&S.full[slot], phase, &S.abort);
+  __device__ __forceinline__ int take(WbSmem& S, bool seen = false) {
+    const bool ok = seen || mbar_wait_short(&S.full[slot], phase, &S.abort);
     tc_fence_after();
     const int off = ok ? slot * (kWfTileBytes >> 4) : -1;
     if (++slot == kWbSlots) {
@@ -307,20 +310,22 @@ __device__ __forceinline__ void window_dkdv(const CUtensorMap& tm_q, const CUten
       const bool more = i + 1 < n;
       int qn = 0, on = 0;
       if (!mbar_wait_short(&S.p_full, i & 1u, &S.abort)) break;
+      bool seen = more && items.probe(S);
       tc_fence_after();
       if (lead) umma_acc(tmem + 256, tmem, rm + o, i == 0);
       if (more) {
-        if ((qn = items.take(S)) < 0) break;
+        if ((qn = items.take(S, seen)) < 0) break;
         if (lead) {
           umma_rows(tmem, kd, rk + qn);
           umma_commit(&S.s_full[0]);
         }
       }
       if (!mbar_wait_short(&S.ds_full, i & 1u, &S.abort)) break;
+      seen = more && items.probe(S);
       tc_fence_after();
       if (lead) umma_acc(tmem + 384, tmem + 128, rm + q, i == 0);
       if (more) {
-        if ((on = items.take(S)) < 0) break;
+        if ((on = items.take(S, seen)) < 0) break;
         if (lead) {
           umma_rows(tmem + 128, vd, rk + on);
           umma_commit(&S.dp_full);
@@ -595,16 +600,16 @@ __device__ __forceinline__ void window_dq(const CUtensorMap& tm_q, const CUtenso
     // its exponentials start.
     WbRing items;
     int k0 = -1, k1 = -1;  // offsets of K of tiles j and j + 1
-    auto issue_s = [&](int j, int& k) {
-      if ((k = items.take(S)) < 0) return false;
+    auto issue_s = [&](int j, int& k, bool seen) {
+      if ((k = items.take(S, seen)) < 0) return false;
       if (lead) {
         umma_rows(tmem + 128u * (j & 1), qdesc, rk + k);
         umma_commit(&S.s_full[j & 1]);
       }
       return true;
     };
-    auto issue_dp = [&] {
-      const int v = items.take(S);
+    auto issue_dp = [&](bool seen) {
+      const int v = items.take(S, seen);
       if (v < 0) return false;
       if (lead) {
         umma_rows(tmem + 256, ddesc, rk + v);
@@ -612,14 +617,21 @@ __device__ __forceinline__ void window_dq(const CUtensorMap& tm_q, const CUtenso
       }
       return true;
     };
-    bool ok = mbar_wait_short(&S.res_full, 0, &S.abort) && issue_s(0, k0) && issue_dp() && (n < 2 || issue_s(1, k1));
+    bool ok = mbar_wait_short(&S.res_full, 0, &S.abort) && issue_s(0, k0, false) && issue_dp(false) &&
+              (n < 2 || issue_s(1, k1, false));
+    bool seen = ok && n > 1 && items.probe(S);
     for (int j = 0; j < n && ok; ++j) {
       if (!mbar_wait_short(&S.ds_full, j & 1u, &S.abort)) break;
       tc_fence_after();
-      if (j + 1 < n && !issue_dp()) break;
+      if (j + 1 < n && !issue_dp(seen)) break;
+      seen = j + 2 < n && items.probe(S);
       if (lead) umma_acc(tmem + 384, tmem + 128u * (j & 1), rm + k0, j == 0);
       k0 = k1;
-      if (j + 2 < n && !issue_s(j + 2, k1)) break;
+      if (j + 2 < n) {
+        const bool s_seen = seen;
+        if (!issue_s(j + 2, k1, s_seen)) break;
+        seen = items.probe(S);
+      }
     }
     if (lead) {
       umma_commit(&S.done);
