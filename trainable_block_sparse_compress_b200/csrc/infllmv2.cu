@@ -345,20 +345,25 @@ BwdLayout bwd_layout(const infllmv2_params* p, int32_t L) {
   return w;
 }
 
-// Row tiles and key splits of the window attention's forward.  A row tile (two 128-row query
-// tiles) is one CTA; when the tiles leave more than half of the SMs idle, the keys of each are
-// split over up to 32 CTAs and joined through the workspace.
+// Row tiles and key splits of the window attention's forward.  A CTA has 256 rows while such tiles
+// keep every SM busy, else 128 rows with the keys shared between its two warpgroups; when even
+// those leave more than half of the SMs idle, the keys of each are split over up to 32 CTAs and
+// joined through the workspace, but not below four key tiles (of `key_tiles`) a CTA: the join
+// costs more than that.
 struct WindowPlan {
-  int row_tiles;
+  int rows, row_tiles;
   long long items;  // row_tiles * B * Hkv
   int n_splits;
 };
-WindowPlan window_plan(const infllmv2_params* p, int32_t Lq) {
+WindowPlan window_plan(const infllmv2_params* p, int32_t Lq, long long key_tiles) {
   WindowPlan d;
-  const int tokens = 256 / (p->num_q_heads / p->num_kv_heads);
-  d.row_tiles = (Lq + tokens - 1) / tokens;
-  d.items = static_cast<long long>(d.row_tiles) * p->batch * p->num_kv_heads;
-  d.n_splits = static_cast<int>(std::max<long long>(1, std::min<long long>(32, num_sms() / d.items)));
+  const int G = p->num_q_heads / p->num_kv_heads;
+  const long long bg = static_cast<long long>(p->batch) * p->num_kv_heads;
+  d.rows = (Lq + 256 / G - 1) / (256 / G) * bg >= num_sms() ? 256 : 128;
+  d.row_tiles = (Lq + d.rows / G - 1) / (d.rows / G);
+  d.items = d.row_tiles * bg;
+  d.n_splits = static_cast<int>(
+      std::max<long long>(1, std::min(std::min<long long>(32, key_tiles / 4), num_sms() / d.items)));
   return d;
 }
 
@@ -447,8 +452,8 @@ size_t ws_size(const infllmv2_params* p, int op, int32_t L) {
       return static_cast<size_t>(norm_rope_grid(p, L, kNrBwdCtas, kNrBwdWaves, &a)) * kHeadDim * sizeof(float);
     }
     case INFLLMV2_OP_WINDOW_ATTN: {
-      const WindowPlan d = window_plan(p, L);
-      return d.n_splits == 1 ? 0 : static_cast<size_t>(d.items) * d.n_splits * 256 * (kHeadDim + 1) * sizeof(float);
+      const WindowPlan d = window_plan(p, L, 1 << 30);  // for every window
+      return d.n_splits == 1 ? 0 : static_cast<size_t>(d.items) * d.n_splits * d.rows * (kHeadDim + 1) * sizeof(float);
     }
     case INFLLMV2_OP_WINDOW_DECODE: {  // for every window and n_sink: window_decode_plan's chunks at most
       const size_t items = static_cast<size_t>(p->batch) * p->num_kv_heads, segs = num_blocks(L) + 1;
@@ -662,15 +667,19 @@ bool sink_maps(const WinParams& w, const CUtensorMap& tk, const CUtensorMap& tv,
 
 // Forward of the window attention on the tensor cores.
 int launch_window(const infllmv2_params* p, const WinParams& w, void* ws, cudaStream_t s) {
-  const WindowPlan d = window_plan(p, w.Lq);
+  const long long tokens = std::min<long long>(w.Lq, 256 / w.G);  // of a CTA
+  const long long keys = std::min<long long>(w.Lmax, std::min<long long>(w.Lmax, static_cast<long long>(w.window) + tokens) +
+                                                         std::min<long long>(w.Lmax, w.n_sink));
+  const WindowPlan d = window_plan(p, w.Lq, (keys + 127) / 128);
   WinTcParams a;
+  a.rows = d.rows;
   a.w = w;
   a.g_log2 = 0;
   while ((1 << a.g_log2) < w.G) ++a.g_log2;
   a.row_tiles = d.row_tiles;
   a.n_splits = d.n_splits;
   a.part_o = static_cast<float*>(ws);
-  a.part_lse = d.n_splits > 1 ? a.part_o + static_cast<size_t>(d.items) * d.n_splits * 256 * kHeadDim : nullptr;
+  a.part_lse = d.n_splits > 1 ? a.part_o + static_cast<size_t>(d.items) * d.n_splits * d.rows * kHeadDim : nullptr;
   const uint64_t items = static_cast<uint64_t>(w.B) * w.Hkv;
   CUtensorMap tq, tk, tv, tks, tvs;
   if (!make_q_map_3d(&tq, w.q, static_cast<uint64_t>(w.B) * w.Lq, w.Hq, w.G) ||
@@ -678,13 +687,15 @@ int launch_window(const infllmv2_params* p, const WinParams& w, void* ws, cudaSt
       !sink_maps(w, tk, tv, &tks, &tvs))
     return INFLLMV2_ERR_CUDA;
   const size_t smem = window_tc_smem_bytes();
-  int st = set_smem(reinterpret_cast<const void*>(window_tc_kernel), smem);
-  if (st != INFLLMV2_OK) return st;
-  window_tc_kernel<<<static_cast<unsigned>(d.items * d.n_splits), kWfThreads, smem, s>>>(tq, tk, tv, tks, tvs, a);
-  if ((st = launch_status()) != INFLLMV2_OK || d.n_splits == 1) return st;
+  auto run = [&](auto kern) {
+    const int st = set_smem(reinterpret_cast<const void*>(kern), smem);
+    if (st != INFLLMV2_OK) return st;
+    return launch_pdl(kern, dim3(static_cast<unsigned>(d.items * d.n_splits)), kWfThreads, smem, s, tq, tk, tv, tks, tvs, a);
+  };
+  const int st = d.rows == 128 ? run(window_tc_kernel<true>) : run(window_tc_kernel<false>);
+  if (st != INFLLMV2_OK || d.n_splits == 1) return st;
   const long long rows = static_cast<long long>(w.B) * w.Lq * w.Hq;
-  window_merge_kernel<<<static_cast<unsigned>((rows + 7) / 8), 256, 0, s>>>(a);
-  return launch_status();
+  return launch_pdl(window_merge_kernel, dim3(static_cast<unsigned>((rows + 7) / 8)), 256, 0, s, a);
 }
 
 int launch_window_decode(const infllmv2_params* p, const WinParams& w, void* ws, cudaStream_t s) {
@@ -745,16 +756,18 @@ int launch_window_backward(const infllmv2_params* p, const WinParams& w, void* w
   const long long dq_ctas = static_cast<long long>(items) * a.row_tiles;
   if (delta_items > 0x7fffffffLL || ctas + dq_ctas > 0x7fffffffLL || items > 65535) return INFLLMV2_ERR_UNSUPPORTED;
   a.kv_items = static_cast<int>(ctas);
-  window_delta_kernel<<<static_cast<unsigned>(std::min<long long>((delta_items + 15) / 16, 64LL * num_sms())), 256, 0, s>>>(a);
-  window_bwd_tc_kernel<<<static_cast<unsigned>(ctas + dq_ctas), kWbThreads, smem, s>>>(tq, tdo, tk, tv, tks, tvs, a);
-  if ((st = launch_status()) != INFLLMV2_OK) return st;
+  const dim3 delta_grid(static_cast<unsigned>(std::min<long long>((delta_items + 15) / 16, 64LL * num_sms())));
+  if ((st = launch_pdl(window_delta_kernel, delta_grid, 256, 0, s, a)) != INFLLMV2_OK) return st;
+  st = launch_pdl(window_bwd_tc_kernel, dim3(static_cast<unsigned>(ctas + dq_ctas)), kWbThreads, smem, s, tq, tdo, tk, tv,
+                  tks, tvs, a);
+  if (st != INFLLMV2_OK) return st;
   const int first = d.chunks_s > 1 ? 0 : d.sink_tiles;
   const int split = d.chunks_w > 1 ? d.key_tiles - first : (d.chunks_s > 1 ? d.sink_tiles : 0);
   if (split > 0) {
     const dim3 grid(static_cast<unsigned>(split) * (2 * kWbKeys / 8), static_cast<unsigned>(items));
-    window_dkdv_merge_kernel<<<grid, 256, 0, s>>>(a, first, split);
+    return launch_pdl(window_dkdv_merge_kernel, grid, 256, 0, s, a, first, split);
   }
-  return launch_status();
+  return INFLLMV2_OK;
 }
 
 int launch_attn(const infllmv2_params* p, const void* q, uint64_t q_rows, const void* k, const void* v,

@@ -60,6 +60,8 @@ struct WinBwdParams {
 __global__ void __launch_bounds__(256) window_delta_kernel(const WinBwdParams p) {
   const WinParams& w = p.w;
   const int l = threadIdx.x & 15;
+  allow_dependent_launch();
+  grid_dependency_wait();
   const unsigned groups = (static_cast<unsigned>(w.Hq) + 3) / 4, items = static_cast<unsigned>(w.B) * p.Lp * groups;
   for (unsigned base = blockIdx.x * 16 + (threadIdx.x >> 5) * 2; base < items; base += gridDim.x * 16) {
     const unsigned it = min(base + ((threadIdx.x >> 4) & 1), items - 1);  // an odd count: the last twice
@@ -456,6 +458,7 @@ __global__ void __launch_bounds__(256) window_dkdv_merge_kernel(const WinBwdPara
   const int lane = threadIdx.x & 31;
   const int row = blockIdx.x * 8 + (threadIdx.x >> 5);
   const int ti = row / (2 * kWbKeys), which = row / kWbKeys & 1, key = row & (kWbKeys - 1);
+  grid_dependency_wait();
   if (ti >= tiles) return;
   const int tile = first_tile + ti, bg = blockIdx.y, b = bg / w.Hkv;
   const int len = chunk_lens(w.q_lens, w.kv_lens, b, w.Lq, w.Lmax).q_len;
@@ -720,6 +723,8 @@ __global__ void __launch_bounds__(kWbThreads, 1)
                          const WinBwdParams p) {
   extern __shared__ __align__(1024) unsigned char smem_1k[];
   const int cta = static_cast<int>(blockIdx.x);
+  allow_dependent_launch();
+  grid_dependency_wait();
   if (cta < p.kv_items)
     window_dkdv(tm_q, tm_do, tm_k, tm_v, p, smem_1k, cta);
   else

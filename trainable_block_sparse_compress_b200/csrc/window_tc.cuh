@@ -141,13 +141,17 @@ struct WinRuns {
 struct WinTcParams {
   WinParams w;
   int g_log2;          // log2 of the group size
-  int row_tiles;       // 256-row tiles per (sequence, kv-head)
+  int rows;            // rows of a CTA: 256, or 128 (paired)
+  int row_tiles;       // tiles of that many rows per (sequence, kv-head)
   int n_splits;        // key splits of a row tile (1: O and lse are written directly)
-  float* part_o;       // splits: [CTA][256][128] normalised partial outputs
-  float* part_lse;     // [CTA][256] base-2 log-sum-exps (-inf: no key)
+  float* part_o;       // splits: [CTA][rows][128] normalised partial outputs
+  float* part_lse;     // [CTA][rows] base-2 log-sum-exps (-inf: no key)
 };
 
 // grid = row_tiles * B * Hkv * n_splits (the last row tiles, which see the most keys, first).
+// kPaired, for calls of few rows: the CTA has one 128-row query tile, and x is not a query tile
+// but every other key tile; the two states are joined through shared memory at the end.
+template <bool kPaired>
 __global__ void __launch_bounds__(kWfThreads, 1)
     window_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_ks,
@@ -167,11 +171,14 @@ __global__ void __launch_bounds__(kWfThreads, 1)
   const int tile = p.row_tiles - 1 - bid / (w.B * w.Hkv);
   const int b = bg / w.Hkv, g = bg - b * w.Hkv;
   const int tt = 128 >> p.g_log2;  // tokens of a 128-row tile
-  const int r0 = tile * 2 * tt;
+  const int ct = kPaired ? tt : 2 * tt;  // tokens of the CTA
+  const int r0 = tile * ct;
+  grid_dependency_wait();
+  allow_dependent_launch();
   const ChunkLens c = chunk_lens(w.q_lens, w.kv_lens, b, w.Lq, w.Lmax);
   if (r0 >= c.q_len) return;
   const int pos0 = c.kv_len - c.q_len;
-  const WinRuns runs(pos0 + r0, pos0 + min(r0 + 2 * tt, c.q_len) - 1, w.window, w.n_sink);
+  const WinRuns runs(pos0 + r0, pos0 + min(r0 + ct, c.q_len) - 1, w.window, w.n_sink);
   // key tiles of this split, and of each query tile within them
   const int all = runs.tiles(), per = (all + p.n_splits - 1) / p.n_splits;
   const int j0 = min(split * per, all), j1 = min(j0 + per, all);
@@ -183,8 +190,14 @@ __global__ void __launch_bounds__(kWfThreads, 1)
     const int end = (runs.ns + (pos0 + rb - runs.lo) / kWfSeg) / 2 + 1;
     jb[x] = max(j0, skip);
     je[x] = ra < c.q_len ? min(j1, end) : 0;
+    if (kPaired) {
+      jb[x] = j0 + x;
+      je[x] = j1;
+    }
     if (je[x] <= jb[x]) jb[x] = je[x] = 0;
   }
+  constexpr int kStep = kPaired ? 2 : 1;  // x takes the key tiles jb[x], jb[x] + kStep, ... < je[x]
+  auto takes = [&](int x, int j) { return j >= jb[x] && j < je[x] && (!kPaired || ((j - jb[x]) & 1) == 0); };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kWfSlots; ++s) mbar_init(&S.full[s], 1);
@@ -215,7 +228,7 @@ __global__ void __launch_bounds__(kWfThreads, 1)
   if (warp == kWfTmaWarp) {
     // ------------------------------------------------------------------ TMA producer
     if (lane == 0) {
-      for (int x = 0; x < 2; ++x)
+      for (int x = 0; x < (kPaired ? 1 : 2); ++x)
         if (je[x] > jb[x]) {
           mbar_arrive_expect_tx(&S.q_full[x], kWfTileBytes);
           for (int h = 0; h < 2; ++h)
@@ -274,7 +287,7 @@ __global__ void __launch_bounds__(kWfThreads, 1)
         if (++slot == kWfSlots) slot = 0;
       }
     if (S.abort && lane == 0) {  // let every copy this thread issued land before the CTA ends
-      for (int x = 0; x < 2; ++x)
+      for (int x = 0; x < (kPaired ? 1 : 2); ++x)
         if (je[x] > jb[x]) mbar_wait_drain(&S.q_full[x], 0);
       for (int s = 0; s < kWfSlots; ++s)
         if (issued > s) mbar_wait_drain(&S.full[s], static_cast<uint32_t>((issued - 1 - s) / kWfSlots) & 1u);
@@ -296,9 +309,8 @@ __global__ void __launch_bounds__(kWfThreads, 1)
     auto need = [&](bool seen, uint64_t* bar, uint32_t parity) {
       if (ok && !seen) ok = mbar_wait_short(bar, parity, &S.abort);
     };
-    for (int x = 0; x < 2; ++x)
+    for (int x = 0; x < (kPaired ? 1 : 2); ++x)
       if (je[x] > jb[x]) need(false, &S.q_full[x], 0);
-    uint32_t np0 = 0, np1 = 0;  // probability tiles consumed per query tile
     int slot = 0;               // ring position of the next item (K of a tile, then its V)
     uint32_t phase = 0;
     auto advance = [&] {
@@ -307,7 +319,8 @@ __global__ void __launch_bounds__(kWfThreads, 1)
         phase ^= 1u;
       }
     };
-    // O_x += P_x V and S_x = Q_x K of the next tile.  `then` probes a barrier needed after it.
+    uint32_t np0 = 0, np1 = 0;  // probability tiles consumed
+    // O_x += P_x V (with P number np of x) and S_x = Q_x K of the next tile.
     auto run_tile = [&](int x, uint32_t& np, bool pv, bool qk, bool p_seen, uint64_t v, uint64_t k, uint64_t* kbar,
                         uint32_t kphase, bool k_known) {
       bool k_seen = k_known;
@@ -325,15 +338,14 @@ __global__ void __launch_bounds__(kWfThreads, 1)
       if (qk) {
         need(k_seen, kbar, kphase);
         if (ok && lead) {
-          umma_rows(tmem + 128u * x, qd + x * (kWfTileBytes >> 4), k);
+          umma_rows(tmem + 128u * x, qd + (kPaired ? 0 : x) * (kWfTileBytes >> 4), k);
           umma_commit(&S.s_full[x]);
         }
       }
     };
     for (int j = j0 - 1; j < j1 && ok; ++j) {
-      const bool pv0 = j >= jb[0] && j < je[0], qk0 = j + 1 >= jb[0] && j + 1 < je[0];
-      const bool pv1 = j >= jb[1] && j < je[1], qk1 = j + 1 >= jb[1] && j + 1 < je[1];
-      const bool p0 = pv0 && mbar_test(&S.p_full[0][0], np0 & 1u);
+      const bool pv0 = takes(0, j), qk0 = takes(0, j + 1), pv1 = takes(1, j), qk1 = takes(1, j + 1);
+      const bool p0 = !kPaired && pv0 && mbar_test(&S.p_full[0][0], np0 & 1u);
       uint64_t v = vd, k = kd;
       if (j >= j0) {
         need(false, &S.full[slot], phase);  // V came with the K read a step ago: seen at once
@@ -347,9 +359,16 @@ __global__ void __launch_bounds__(kWfThreads, 1)
         k += static_cast<uint32_t>(slot) * (kWfTileBytes >> 4);
         advance();
       }
-      run_tile(0, np0, pv0, qk0, p0, v, k, kbar, kphase, false);
-      const bool p1 = pv1 && mbar_test(&S.p_full[1][0], np1 & 1u);
-      run_tile(1, np1, pv1, qk1, p1, v, k, kbar, kphase, qk0);
+      if (kPaired) {  // the next tile's scores first: they go to the other buffer
+        if (qk0) run_tile(0, np0, false, true, false, v, k, kbar, kphase, false);
+        if (qk1) run_tile(1, np1, false, true, false, v, k, kbar, kphase, false);
+        if (pv0) run_tile(0, np0, true, false, false, v, k, kbar, kphase, true);
+        if (pv1) run_tile(1, np1, true, false, false, v, k, kbar, kphase, true);
+      } else {
+        run_tile(0, np0, pv0, qk0, p0, v, k, kbar, kphase, false);
+        const bool p1 = pv1 && mbar_test(&S.p_full[1][0], np1 & 1u);
+        run_tile(1, np1, pv1, qk1, p1, v, k, kbar, kphase, qk0);
+      }
       if (ok && has_k && !qk0 && !qk1) need(false, kbar, kphase);  // its slot is released below all the same
       if (ok && lead) umma_commit(&S.step[(j + 1 - j0) & 1]);  // V of tile j and K of tile j + 1 have been read
       __syncwarp();
@@ -369,17 +388,18 @@ __global__ void __launch_bounds__(kWfThreads, 1)
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWfSoftRegs));
   const int x = warp >> 2;
   const int row = threadIdx.x & 127;
-  const int r = r0 + x * tt + (row >> p.g_log2);
+  const int rx = kPaired ? r0 : r0 + x * tt;  // first token of the warpgroup's rows
+  const int r = rx + (row >> p.g_log2);
   const bool valid = r < c.q_len;
   const bool warp_live = __any_sync(0xffffffffu, valid);
   const int t = pos0 + min(r, c.q_len - 1);
-  const int tx_min = pos0 + r0 + x * tt, tx_max = pos0 + min(r0 + (x + 1) * tt, c.q_len) - 1;
+  const int tx_min = pos0 + rx, tx_max = pos0 + min(rx + tt, c.q_len) - 1;
   const uint32_t tl = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
   const uint32_t ts = tl + 128u * x, to = tl + kWfColO + 128u * x;
   const float sl2 = w.scale_log2;
   float m2 = -INFINITY, sum = 0.f;  // reference maximum (scaled, base 2) and sum of the row
   uint32_t n = 0;
-  for (int j = jb[x]; j < je[x]; ++j, ++n) {
+  for (int j = jb[x]; j < je[x]; j += kStep, ++n) {
     mbar_wait_short(&S.s_full[x], n & 1u, &S.abort);  // after a timeout the loop runs on: its loads are collective
     tc_fence_after();
     if (warp_live) {
@@ -458,29 +478,68 @@ __global__ void __launch_bounds__(kWfThreads, 1)
   }
   mbar_wait_short(&S.mma_done, 0, &S.abort);
   tc_fence_after();
-  if (warp_live) {
+  // paired: the second warpgroup leaves its state in the ring (every product has read it), as
+  // [16-byte column][row] so that a warp's accesses are consecutive
+  float4* joint = reinterpret_cast<float4*>(ring);
+  float2* joint_ms = reinterpret_cast<float2*>(joint + 32 * 128);
+  float f_own = 1.f, f_other = 0.f;
+  if (kPaired) {
+    if (x == 1) {
+      joint_ms[row] = make_float2(n > 0 ? m2 : -INFINITY, sum);
+      if (warp_live && n > 0)
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          uint32_t v[32];
+          tmem_ld32(to + 32 * q, v);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            joint[(8 * q + i) * 128 + row] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
+                                                         __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]));
+        }
+    }
+    named_bar_sync(2, 256);
+    if (x == 0) {
+      const float2 o = joint_ms[row];
+      const float mn = fmaxf(m2, o.x);
+      f_own = m2 == -INFINITY ? 0.f : ex2(m2 - mn);
+      f_other = o.x == -INFINITY ? 0.f : ex2(o.x - mn);  // 0 also where that state has no tile
+      sum = sum * f_own + (f_other > 0.f ? o.y * f_other : 0.f);
+      m2 = mn;
+    }
+  }
+  if (warp_live && (!kPaired || x == 0)) {
     const int h = (g << p.g_log2) + (row & ((1 << p.g_log2) - 1));
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
     const float lse2 = sum > 0.f ? m2 + lg2(sum) : -INFINITY;
     const size_t orow = (static_cast<size_t>(b) * w.Lq + r) * w.Hq + h;
-    const size_t prow = (static_cast<size_t>(blockIdx.x) * 2 + x) * 128 + row;
+    const size_t prow = static_cast<size_t>(blockIdx.x) * p.rows + x * 128 + row;
     if (valid) {
       if (p.n_splits > 1)
         p.part_lse[prow] = lse2;
       else if (w.lse)
         w.lse[(static_cast<size_t>(b) * w.Hq + h) * w.Lq + r] = lse2 * 0.6931471805599453f;
     }
+    const float inv_own = inv * f_own, inv_other = inv * f_other;
     if (n > 0)
 #pragma unroll 1
       for (int q = 0; q < 4; ++q) {
         uint32_t v[32];
         tmem_ld32(to + 32 * q, v);
-        if (valid && p.n_splits > 1) {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + prow * kHeadDim + 32 * q);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            dst[i] = make_float4(__uint_as_float(v[4 * i]) * inv, __uint_as_float(v[4 * i + 1]) * inv,
-                                 __uint_as_float(v[4 * i + 2]) * inv, __uint_as_float(v[4 * i + 3]) * inv);
+        for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * inv_own);
+        if (kPaired && inv_other > 0.f)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float4 o = joint[(8 * q + i) * 128 + row];
+            v[4 * i] = __float_as_uint(fmaf(o.x, inv_other, __uint_as_float(v[4 * i])));
+            v[4 * i + 1] = __float_as_uint(fmaf(o.y, inv_other, __uint_as_float(v[4 * i + 1])));
+            v[4 * i + 2] = __float_as_uint(fmaf(o.z, inv_other, __uint_as_float(v[4 * i + 2])));
+            v[4 * i + 3] = __float_as_uint(fmaf(o.w, inv_other, __uint_as_float(v[4 * i + 3])));
+          }
+        if (valid && p.n_splits > 1) {
+          uint4* dst = reinterpret_cast<uint4*>(p.part_o + prow * kHeadDim + 32 * q);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) dst[i] = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
         } else if (valid) {
           uint4* dst = reinterpret_cast<uint4*>(w.o + orow * kHeadDim + 32 * q);
 #pragma unroll
@@ -488,7 +547,7 @@ __global__ void __launch_bounds__(kWfThreads, 1)
             uint32_t u[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              u[e] = pack_bf16(__uint_as_float(v[8 * i + 2 * e]) * inv, __uint_as_float(v[8 * i + 2 * e + 1]) * inv);
+              u[e] = pack_bf16(__uint_as_float(v[8 * i + 2 * e]), __uint_as_float(v[8 * i + 2 * e + 1]));
             dst[i] = make_uint4(u[0], u[1], u[2], u[3]);
           }
         }
@@ -505,23 +564,24 @@ __global__ void __launch_bounds__(256) window_merge_kernel(const WinTcParams p) 
   const WinParams& w = p.w;
   const int lane = threadIdx.x & 31;
   const long long row = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  grid_dependency_wait();
   if (row >= static_cast<long long>(w.B) * w.Lq * w.Hq) return;
   const int h = static_cast<int>(row % w.Hq), r = static_cast<int>(row / w.Hq % w.Lq);
   const int b = static_cast<int>(row / w.Hq / w.Lq);
   const ChunkLens c = chunk_lens(w.q_lens, w.kv_lens, b, w.Lq, w.Lmax);
   if (r >= c.q_len) return;
-  const int tt = 128 >> p.g_log2, tile = r / (2 * tt);
+  const int ct = p.rows >> p.g_log2, tile = r / ct;
   const int bg = b * w.Hkv + (h >> p.g_log2);
   const size_t cta = (static_cast<size_t>(p.row_tiles - 1 - tile) * w.B * w.Hkv + bg) * p.n_splits;
-  const size_t in = static_cast<size_t>(r - tile * 2 * tt) * w.G + (h & (w.G - 1));  // row of the CTA's 256
+  const size_t in = static_cast<size_t>(r - tile * ct) * w.G + (h & (w.G - 1));  // row of the CTA
   float mx = -INFINITY;
-  for (int s = 0; s < p.n_splits; ++s) mx = fmaxf(mx, p.part_lse[(cta + s) * 256 + in]);
+  for (int s = 0; s < p.n_splits; ++s) mx = fmaxf(mx, p.part_lse[(cta + s) * p.rows + in]);
   float acc[4] = {0.f, 0.f, 0.f, 0.f}, z = 0.f;
   for (int s = 0; s < p.n_splits; ++s) {
-    const float l = p.part_lse[(cta + s) * 256 + in];
+    const float l = p.part_lse[(cta + s) * p.rows + in];
     if (l == -INFINITY) continue;
     const float e = ex2(l - mx);
-    const float4 o = *(reinterpret_cast<const float4*>(p.part_o + ((cta + s) * 256 + in) * kHeadDim) + lane);
+    const float4 o = *(reinterpret_cast<const float4*>(p.part_o + ((cta + s) * p.rows + in) * kHeadDim) + lane);
     z += e;
     acc[0] = fmaf(e, o.x, acc[0]), acc[1] = fmaf(e, o.y, acc[1]);
     acc[2] = fmaf(e, o.z, acc[2]), acc[3] = fmaf(e, o.w, acc[3]);
