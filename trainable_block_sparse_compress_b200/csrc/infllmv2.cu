@@ -383,13 +383,13 @@ WindowDecodePlan window_decode_plan(const infllmv2_params* p, int32_t Lmax, int3
   return {static_cast<int>(per), static_cast<int>((segs + per - 1) / per)};
 }
 // Backward of the window attention: cuts of the key tiles' query ranges (counted for sequences
-// of L tokens).  A key tile of a long range (one that holds sinks, or any while key tiles are
-// fewer than SMs) is cut into chunks of q_tiles query tiles, at least 16 (their partials cost a
-// write and a read of 128 KB), at most so many that kWbMaxParts partials hold them.
+// of L tokens).  The aim is two CTAs of equal work an SM, at least 16 query tiles each (a partial
+// costs a write and a read of 128 KB): a kind of key tile whose range is n such shares, rounded,
+// is cut into n chunks, unless that needs more than kWbMaxParts partials (then the shares grow).
 constexpr int kWbMaxParts = 512;
 constexpr size_t kWbPartBytes = 2 * kWbKeys * kHeadDim * sizeof(float);
 struct WindowBwdPlan {
-  int key_tiles, sink_tiles, q_tiles, chunks_s, chunks_w;
+  int key_tiles, sink_tiles, chunks_s, chunks_w, q_tiles_s, q_tiles_w;
   long long parts;  // partials of all (sequence, kv-head)s
   size_t lse2, delta, part, total;
 };
@@ -409,13 +409,14 @@ WindowBwdPlan window_bwd_plan(const infllmv2_params* p, int32_t L, int32_t windo
   }
   long long q = std::max<long long>(16, visits * items / (2 * num_sms()) + 1);
   for (;; q += q / 4) {
-    d.chunks_s = static_cast<int>(std::max<long long>(1, (longest[1] + q - 1) / q));
-    d.chunks_w = static_cast<int>(std::max<long long>(1, (longest[0] + q - 1) / q));
+    d.chunks_s = static_cast<int>(std::max<long long>(1, (longest[1] + q / 2) / q));
+    d.chunks_w = static_cast<int>(std::max<long long>(1, (longest[0] + q / 2) / q));
     d.parts = items * ((d.chunks_s > 1 ? static_cast<long long>(d.sink_tiles) * d.chunks_s : 0) +
                        (d.chunks_w > 1 ? static_cast<long long>(d.key_tiles - d.sink_tiles) * d.chunks_w : 0));
     if (d.parts <= kWbMaxParts) break;
   }
-  d.q_tiles = static_cast<int>(std::min<long long>(q, 1 << 30));
+  d.q_tiles_s = static_cast<int>(std::max<long long>(1, (longest[1] + d.chunks_s - 1) / d.chunks_s));
+  d.q_tiles_w = static_cast<int>(std::max<long long>(1, (longest[0] + d.chunks_w - 1) / d.chunks_w));
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   const size_t stats = up(static_cast<size_t>(p->batch) * p->num_q_heads * d.key_tiles * kWbKeys * sizeof(float));
   d.lse2 = 0;
@@ -739,7 +740,8 @@ int launch_window_backward(const infllmv2_params* p, const WinParams& w, void* w
   a.sink_tiles = d.sink_tiles;
   a.chunks_s = d.chunks_s;
   a.chunks_w = d.chunks_w;
-  a.q_tiles = d.q_tiles;
+  a.q_tiles_s = d.q_tiles_s;
+  a.q_tiles_w = d.q_tiles_w;
   a.row_tiles = (w.Lq * w.G + 127) / 128;
   const uint64_t items = static_cast<uint64_t>(w.B) * w.Hkv;
   CUtensorMap tq, tdo, tk, tv, tks, tvs;

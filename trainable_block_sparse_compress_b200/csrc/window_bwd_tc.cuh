@@ -15,7 +15,7 @@
 // S and dP are computed in both (7 products instead of 5): that keeps dq out of fp32 atomics
 // (its order of sums is fixed) and of a 4-byte accumulator in HBM.
 // A tile of keys that holds sinks is seen by every later query: its query range (and any
-// other, when there are few tiles of keys) is cut into chunks of q_tiles query tiles whose
+// other, when there are few tiles of keys) is cut into chunks of query tiles whose
 // partial sums meet in the workspace; window_dkdv_merge_kernel adds them in order.
 #pragma once
 #include "common.cuh"
@@ -32,7 +32,7 @@ constexpr int kWbSlots = 5;
 constexpr int kWbKeys = 128;  // keys of a dK / dV tile
 
 struct WbSmem {
-  uint64_t res_full, full[kWbSlots], s_full[2], dp_full, p_full, ds_full, done, mma_done, tail[2];
+  uint64_t res_full, full[kWbSlots], s_full, dp_full, p_full, ds_full, free_[2], done, mma_done, tail[2];
   uint64_t st_full[2], st_empty[2];
   alignas(16) float stats[2][2][128];  // dK / dV: lse and D of a query tile's rows
   uint32_t tmem_base;
@@ -48,9 +48,9 @@ struct WinBwdParams {
   WinParams w;
   int g_log2, Lp;       // Lp: tokens padded to a multiple of 128
   float *lse2, *delta;  // [B, Hkv, Lp, G]: -lse in base 2 and -D
-  // dK / dV: key tiles 0 .. sink_tiles-1 have chunks_s chunks of q_tiles query tiles, the others
-  // chunks_w; a kind with more than one chunk goes through the partials
-  int key_tiles, sink_tiles, chunks_s, chunks_w, q_tiles, row_tiles;
+  // dK / dV: key tiles 0 .. sink_tiles-1 have chunks_s chunks of q_tiles_s query tiles, the others
+  // chunks_w of q_tiles_w; a kind with more than one chunk goes through the partials
+  int key_tiles, sink_tiles, chunks_s, chunks_w, q_tiles_s, q_tiles_w, row_tiles;
   int kv_items;         // CTAs of the dK / dV part
   float* part;          // [chunk slot][dV, dK][128 keys][128]
 };
@@ -187,7 +187,8 @@ __device__ __forceinline__ void window_dkdv(const CUtensorMap& tm_q, const CUten
   if (u0 >= len) return;
   const int t_end = window_t_end(w, tile, len);
   const int n_all = (t_end - u0 + tt - 1) / tt;
-  const int i0 = chunk * p.q_tiles, i1 = chunks == 1 ? n_all : min(n_all, i0 + p.q_tiles);
+  const int q_tiles = sink_kind ? p.q_tiles_s : p.q_tiles_w;
+  const int i0 = chunk * q_tiles, i1 = chunks == 1 ? n_all : min(n_all, i0 + q_tiles);
   if (i0 >= i1) return;
   const int n = i1 - i0;
   const int ta = u0 + i0 * tt;  // first token
@@ -196,11 +197,11 @@ __device__ __forceinline__ void window_dkdv(const CUtensorMap& tm_q, const CUten
     mbar_init(&S.res_full, 1);
     for (int s = 0; s < kWbSlots; ++s) mbar_init(&S.full[s], 1);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&S.s_full[s], 1);
       mbar_init(&S.tail[s], 1);
       mbar_init(&S.st_full[s], 1);
       mbar_init(&S.st_empty[s], kWbEltWarps);
     }
+    mbar_init(&S.s_full, 1);
     mbar_init(&S.p_full, kWbEltWarps);
     mbar_init(&S.ds_full, kWbEltWarps);
     mbar_init(&S.dp_full, 1);
@@ -300,7 +301,7 @@ __device__ __forceinline__ void window_dkdv(const CUtensorMap& tm_q, const CUten
     if (ok) {
       if (lead) {
         umma_rows(tmem, kd, rk + q);
-        umma_commit(&S.s_full[0]);
+        umma_commit(&S.s_full);
       }
       ok = (o = items.take(S)) >= 0;
     }
@@ -319,7 +320,7 @@ __device__ __forceinline__ void window_dkdv(const CUtensorMap& tm_q, const CUten
         if ((qn = items.take(S, seen)) < 0) break;
         if (lead) {
           umma_rows(tmem, kd, rk + qn);
-          umma_commit(&S.s_full[0]);
+          umma_commit(&S.s_full);
         }
       }
       if (!mbar_wait_short(&S.ds_full, i & 1u, &S.abort)) break;
@@ -364,7 +365,7 @@ __device__ __forceinline__ void window_dkdv(const CUtensorMap& tm_q, const CUten
     const float4* st = reinterpret_cast<const float4*>(S.stats[i & 1][0] + 32 * wg);
     const float4* sd = reinterpret_cast<const float4*>(S.stats[i & 1][1] + 32 * wg);
     mbar_wait_short(&S.st_full[i & 1], static_cast<uint32_t>(i >> 1) & 1u, &S.abort);
-    mbar_wait_short(&S.s_full[0], i & 1u, &S.abort);
+    mbar_wait_short(&S.s_full, i & 1u, &S.abort);
     tc_fence_after();
     uint32_t v[32];
     tmem_ld32_nowait(tl, v);
@@ -469,7 +470,8 @@ __global__ void __launch_bounds__(256) window_dkdv_merge_kernel(const WinBwdPara
   const int slot0 = sink ? tile * chunks : (p.chunks_s > 1 ? p.sink_tiles * p.chunks_s : 0) + (tile - p.sink_tiles) * chunks;
   const int tt = 128 >> p.g_log2;
   const int n_all = (window_t_end(w, tile, len) - tile * kWbKeys + tt - 1) / tt;
-  const int live = min(chunks, (n_all + p.q_tiles - 1) / p.q_tiles);
+  const int q_tiles = sink ? p.q_tiles_s : p.q_tiles_w;
+  const int live = min(chunks, (n_all + q_tiles - 1) / q_tiles);
   float a[4] = {0.f, 0.f, 0.f, 0.f};
   for (int c = 0; c < live; ++c) {
     const size_t item = static_cast<size_t>(slot0 + c) * (w.B * w.Hkv) + bg;
@@ -482,8 +484,8 @@ __global__ void __launch_bounds__(256) window_dkdv_merge_kernel(const WinBwdPara
   store4((which ? w.dk : w.dv) + (static_cast<size_t>(bg) * w.Lmax + u) * kHeadDim, lane, a);
 }
 
-// One dq item: `cta` of row_tiles * B * Hkv, the last row tiles first.  TMEM: S 0 and 128,
-// dP 256, dQ 384.
+// One dq item: `cta` of row_tiles * B * Hkv, the last row tiles first.  TMEM: S 0, dP 128 (dS
+// over it), dQ 384.
 __device__ __forceinline__ void window_dq(const CUtensorMap& tm_q, const CUtensorMap& tm_do, const CUtensorMap& tm_k,
                                           const CUtensorMap& tm_v, const CUtensorMap& tm_ks, const CUtensorMap& tm_vs,
                                           const WinBwdParams& p, unsigned char* base, int cta) {
@@ -508,9 +510,11 @@ __device__ __forceinline__ void window_dq(const CUtensorMap& tm_q, const CUtenso
     mbar_init(&S.res_full, 1);
     for (int s = 0; s < kWbSlots; ++s) mbar_init(&S.full[s], 1);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&S.s_full[s], 1);
       mbar_init(&S.tail[s], 1);
+      mbar_init(&S.free_[s], 1);
     }
+    mbar_init(&S.s_full, 1);
+    mbar_init(&S.p_full, kWbEltWarps);
     mbar_init(&S.ds_full, kWbEltWarps);
     mbar_init(&S.dp_full, 1);
     mbar_init(&S.done, 1);
@@ -539,14 +543,12 @@ __device__ __forceinline__ void window_dq(const CUtensorMap& tm_q, const CUtenso
     bool tail_used = false, stop = false;
     for (int j = 0; j < n && !stop; ++j)
       for (int kv = 0; kv < 2; ++kv) {
-        // Items 2t + 5 and 2t + 6 take the slots of K and V of tile t, which have been read once S of
-        // tile t + 2 is complete (dQ of tile t and dP of tile t + 1 were issued before it).  The next
-        // S on its barrier, of tile t + 4, waits for later items; S of tile 0 is waited for before S
-        // of tile 2 can start.
-        if (issued == 4) mbar_wait_short(&S.s_full[0], 0, &S.abort);
+        // Items 2t + 5 and 2t + 6 take the slots of K and V of tile t, which have been read once dQ
+        // of tile t is complete.  dQ of tile t + 2 waits for item 2t + 5, so the barrier of tile t
+        // (one of two) is never a phase further.
         if (issued >= kWbSlots && issued % 2 == 1) {
-          const int sj = (issued - kWbSlots) / 2 + 2;
-          mbar_wait_short(&S.s_full[sj & 1], static_cast<uint32_t>(sj >> 1) & 1u, &S.abort);
+          const int t = (issued - kWbSlots) / 2;
+          mbar_wait_short(&S.free_[t & 1], static_cast<uint32_t>(t >> 1) & 1u, &S.abort);
         }
         stop = __any_sync(0xffffffffu, S.abort != 0);
         if (stop) break;
@@ -599,15 +601,15 @@ __device__ __forceinline__ void window_dq(const CUtensorMap& tm_q, const CUtenso
     const bool lead = elect_one();  // as for dK / dV
     const uint64_t qdesc = desc_k_sw128(smem_u32(qd)), ddesc = qdesc + (kWfTileBytes >> 4);
     const uint64_t rk = desc_k_sw128(smem_u32(ring)), rm = desc_mn_sw128(smem_u32(ring), kWfHalf, 1024);
-    // Order: S(0) dP(0) S(1) | dP(j+1) dQ(j) S(j+2): the next tile's scores and dP are there when
-    // its exponentials start.
+    // Order: S(0) dP(0) | S(j+1) | dQ(j) dP(j+1).  S(j+1) starts once the scores of tile j are in
+    // registers and is there when their dS is done; dP(j+1) runs under the exponentials.
     WbRing items;
     int k0 = -1, k1 = -1;  // offsets of K of tiles j and j + 1
-    auto issue_s = [&](int j, int& k, bool seen) {
+    auto issue_s = [&](int& k, bool seen) {
       if ((k = items.take(S, seen)) < 0) return false;
       if (lead) {
-        umma_rows(tmem + 128u * (j & 1), qdesc, rk + k);
-        umma_commit(&S.s_full[j & 1]);
+        umma_rows(tmem, qdesc, rk + k);
+        umma_commit(&S.s_full);
       }
       return true;
     };
@@ -615,26 +617,27 @@ __device__ __forceinline__ void window_dq(const CUtensorMap& tm_q, const CUtenso
       const int v = items.take(S, seen);
       if (v < 0) return false;
       if (lead) {
-        umma_rows(tmem + 256, ddesc, rk + v);
+        umma_rows(tmem + 128, ddesc, rk + v);
         umma_commit(&S.dp_full);
       }
       return true;
     };
-    bool ok = mbar_wait_short(&S.res_full, 0, &S.abort) && issue_s(0, k0, false) && issue_dp(false) &&
-              (n < 2 || issue_s(1, k1, false));
-    bool seen = ok && n > 1 && items.probe(S);
+    bool ok = mbar_wait_short(&S.res_full, 0, &S.abort) && issue_s(k0, false) && issue_dp(false);
     for (int j = 0; j < n && ok; ++j) {
-      if (!mbar_wait_short(&S.ds_full, j & 1u, &S.abort)) break;
+      const bool more = j + 1 < n;
+      bool seen = more && items.probe(S);
+      if (!mbar_wait_short(&S.p_full, j & 1u, &S.abort)) break;  // the scores have been read
       tc_fence_after();
-      if (j + 1 < n && !issue_dp(seen)) break;
-      seen = j + 2 < n && items.probe(S);
-      if (lead) umma_acc(tmem + 384, tmem + 128u * (j & 1), rm + k0, j == 0);
-      k0 = k1;
-      if (j + 2 < n) {
-        const bool s_seen = seen;
-        if (!issue_s(j + 2, k1, s_seen)) break;
-        seen = items.probe(S);
+      if (more && !issue_s(k1, seen)) break;
+      if (!mbar_wait_short(&S.ds_full, j & 1u, &S.abort)) break;
+      seen = more && items.probe(S);
+      tc_fence_after();
+      if (lead) {
+        umma_acc(tmem + 384, tmem + 128, rm + k0, j == 0);
+        umma_commit(&S.free_[j & 1]);
       }
+      k0 = k1;
+      if (more && !issue_dp(seen)) break;
     }
     if (lead) {
       umma_commit(&S.done);
@@ -663,13 +666,16 @@ __device__ __forceinline__ void window_dq(const CUtensorMap& tm_q, const CUtenso
     const bool all = u0 + kWfSeg - 1 <= r0 && t_last == r0 + tt - 1 &&
                      (runs.is_sink(seg) ? u0 + kWfSeg <= w.n_sink
                                         : (u0 > t_last - w.window || u0 + kWfSeg <= w.n_sink));
-    const uint32_t ts = tmem + lane0 + 128u * (j & 1) + 32u * wg, td = tmem + lane0 + 256u + 32u * wg;
-    mbar_wait_short(&S.s_full[j & 1], static_cast<uint32_t>(j >> 1) & 1u, &S.abort);
+    const uint32_t ts = tmem + lane0 + 32u * wg, td = ts + 128u;
+    mbar_wait_short(&S.s_full, j & 1u, &S.abort);
     tc_fence_after();
     uint32_t v[32];
     tmem_ld32_nowait(ts, v);
     uint64_t pr[16];
     tmem_wait_ld_tied(v);
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&S.p_full);  // S may be overwritten
 #pragma unroll
     for (int q = 0; q < 16; ++q)
       pr[q] = ex2_pair(fma2(f2(__uint_as_float(v[2 * q]), __uint_as_float(v[2 * q + 1])), sl2, lse2));
@@ -684,7 +690,7 @@ __device__ __forceinline__ void window_dq(const CUtensorMap& tm_q, const CUtenso
     uint32_t pk[16];
 #pragma unroll
     for (int q = 0; q < 16; ++q) pk[q] = pack_pair(pr[q]);
-    tmem_st16_nowait(ts, pk);
+    tmem_st16_nowait(td, pk);
     tmem_wait_st();
     tc_fence_before();
     __syncwarp();
