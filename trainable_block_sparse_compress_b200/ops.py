@@ -99,12 +99,12 @@ def _need(t: torch.Tensor, name: str, dtype, shape=None):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
-def _workspace(p: Params, op: int, L: int, ws: Optional[torch.Tensor], device) -> Optional[torch.Tensor]:
+def _workspace(p: Params, op: int, L: int, ws: Optional[torch.Tensor], like: torch.Tensor) -> Optional[torch.Tensor]:
     n = workspace_size(p, op, L)
     if n == 0:
         return ws
     if ws is None or ws.numel() * ws.element_size() < n:
-        ws = torch.empty(n, dtype=torch.uint8, device=device)
+        ws = like.new_empty(n, dtype=torch.uint8)
     return ws
 
 
@@ -170,7 +170,7 @@ def select_blocks_decode(p: Params, q: torch.Tensor, kc: torch.Tensor, lens: tor
     if out is None:
         out = torch.empty((p.batch, p.num_kv_heads, 1, p.topk), dtype=torch.int32, device=q.device)
     _need(out, "block_idx", torch.int32, (p.batch, p.num_kv_heads, 1, p.topk))
-    ws = _workspace(p, _lib.OP_SELECT_DECODE, Lmax, ws, q.device)
+    ws = _workspace(p, _lib.OP_SELECT_DECODE, Lmax, ws, q)
     nbytes = 0 if ws is None else ws.numel() * ws.element_size()
     st = _lib.load().infllmv2_select_blocks(ctypes.byref(p.c()), _lib.MODE_DECODE, _ptr(q), _ptr(kc), _ptr(lens),
                                             Lmax, _ptr(out), _ptr(ws), nbytes, _stream())
@@ -245,7 +245,7 @@ def sparse_attn_backward(p: Params, q: torch.Tensor, k: torch.Tensor, v: torch.T
     dq = torch.empty_like(q)
     dk = torch.empty_like(k)
     dv = torch.empty_like(v)
-    ws = _workspace(p, _lib.OP_ATTN_BACKWARD, L, ws, q.device)
+    ws = _workspace(p, _lib.OP_ATTN_BACKWARD, L, ws, q)
     nbytes = ws.numel() * ws.element_size()
     st = _lib.load().infllmv2_sparse_attn_backward(ctypes.byref(p.c()), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse),
                                                    _ptr(d_o), _ptr(block_idx), L, _ptr(dq), _ptr(dk), _ptr(dv),
@@ -272,7 +272,7 @@ def sparse_attn_decode(p: Params, q: torch.Tensor, k_cache: torch.Tensor, v_cach
         lse = torch.empty((p.batch, p.num_q_heads), dtype=torch.float32, device=q.device)
     if lse is not None:
         _need(lse, "lse", torch.float32, (p.batch, p.num_q_heads))
-    ws = _workspace(p, _lib.OP_ATTN_DECODE, Lmax, ws, q.device)
+    ws = _workspace(p, _lib.OP_ATTN_DECODE, Lmax, ws, q)
     nbytes = 0 if ws is None else ws.numel() * ws.element_size()
     st = _lib.load().infllmv2_sparse_attn_decode(ctypes.byref(p.c()), _ptr(q), _ptr(k_cache), _ptr(v_cache),
                                                  _ptr(lens), Lmax, _ptr(block_idx), _ptr(out), _ptr(lse),
@@ -458,7 +458,7 @@ def qk_norm_rope_backward(p: Params, q: torch.Tensor, k: torch.Tensor, d_q: torc
     dq, dk, dv = out[:, :, :Hq], out[:, :, Hq:Hq + Hkv], out[:, :, Hq + Hkv:]
     d_qw = None if q_weight is None else torch.empty(d, dtype=torch.float32, device=q.device)
     d_kw = None if k_weight is None else torch.empty(d, dtype=torch.float32, device=q.device)
-    ws = _workspace(p, _lib.OP_QK_NORM_ROPE_BACKWARD, Lq, ws, q.device)
+    ws = _workspace(p, _lib.OP_QK_NORM_ROPE_BACKWARD, Lq, ws, q)
     nbytes = ws.numel() * ws.element_size()
     rs = (Hq + 2 * Hkv) * d
     st = _lib.load().infllmv2_qk_norm_rope_backward(
@@ -494,7 +494,7 @@ def window_attn_chunk(p: Params, q: torch.Tensor, k: torch.Tensor, v: torch.Tens
         _need(lse, "lse", torch.float32, (B, Hq, Lq))
     elif want_lse:
         lse = q.new_empty((B, Hq, Lq), dtype=torch.float32)
-    ws = _workspace(p, _lib.OP_WINDOW_ATTN, Lq, ws, q.device)
+    ws = _workspace(p, _lib.OP_WINDOW_ATTN, Lq, ws, q)
     nbytes = 0 if ws is None else ws.numel() * ws.element_size()
     st = _lib.load().infllmv2_window_attn(ctypes.byref(p.c()), _ptr(q), Lq, _ptr(k), _ptr(v), _ptr(q_lens),
                                           _ptr(kv_lens), Lmax, window, n_sink, _ptr(out), _ptr(lse), _ptr(ws), nbytes,
@@ -535,7 +535,7 @@ def window_attn_decode(p: Params, q: torch.Tensor, k_cache: torch.Tensor, v_cach
         _need(lse, "lse", torch.float32, (p.batch, p.num_q_heads))
     elif want_lse:
         lse = q.new_empty((p.batch, p.num_q_heads), dtype=torch.float32)
-    ws = _workspace(p, _lib.OP_WINDOW_DECODE, Lmax, ws, q.device)
+    ws = _workspace(p, _lib.OP_WINDOW_DECODE, Lmax, ws, q)
     nbytes = 0 if ws is None else ws.numel() * ws.element_size()
     st = _lib.load().infllmv2_window_attn_decode(ctypes.byref(p.c()), _ptr(q), _ptr(k_cache), _ptr(v_cache),
                                                  _ptr(lens), Lmax, window, n_sink, _ptr(out), _ptr(lse), _ptr(ws),
@@ -566,7 +566,7 @@ def window_attn_backward(p: Params, q: torch.Tensor, k: torch.Tensor, v: torch.T
     dq = torch.empty_like(q) if dq is None else dq
     dk = torch.empty_like(k) if dk is None else dk
     dv = torch.empty_like(v) if dv is None else dv
-    ws = _workspace(p, _lib.OP_WINDOW_BACKWARD, L, ws, q.device)
+    ws = _workspace(p, _lib.OP_WINDOW_BACKWARD, L, ws, q)
     nbytes = 0 if ws is None else ws.numel() * ws.element_size()
     st = _lib.load().infllmv2_window_attn_backward(ctypes.byref(p.c()), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse),
                                                    _ptr(d_o), _ptr(lens), L, window, n_sink, _ptr(dq), _ptr(dk),
