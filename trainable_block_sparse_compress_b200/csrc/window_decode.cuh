@@ -256,19 +256,32 @@ __global__ void __launch_bounds__(128) window_decode_merge_kernel(const WinDecod
   const WinRuns runs(len - 1, len - 1, w.window, w.n_sink);
   const int live = (runs.ns + runs.nw + p.per_chunk - 1) / p.per_chunk;
   const size_t row0 = static_cast<size_t>(b * w.Hkv + (h >> p.g_log2)) * p.chunks * w.G + (h & (w.G - 1));
+  // this warp's first rows are on their way while the maximum is found
+  float4 x[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (warp + 4 * u < live)
+      x[u] = *(reinterpret_cast<const float4*>(p.part_o + (row0 + static_cast<size_t>(warp + 4 * u) * w.G) * kHeadDim) + lane);
+  }
   float mx = -INFINITY;
   for (int c = lane; c < live; c += 32) mx = fmaxf(mx, p.part_lse[row0 + static_cast<size_t>(c) * w.G]);
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
   float acc[4] = {0.f, 0.f, 0.f, 0.f}, z = 0.f;
-#pragma unroll 4
-  for (int c = warp; c < live; c += 4) {
-    const size_t pr = row0 + static_cast<size_t>(c) * w.G;
-    const float e = ex2(p.part_lse[pr] - mx);
-    const float4 x = *(reinterpret_cast<const float4*>(p.part_o + pr * kHeadDim) + lane);
-    z += e;
-    acc[0] = fmaf(e, x.x, acc[0]), acc[1] = fmaf(e, x.y, acc[1]);
-    acc[2] = fmaf(e, x.z, acc[2]), acc[3] = fmaf(e, x.w, acc[3]);
+  for (int c0 = warp; c0 < live; c0 += 16) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int c = c0 + 4 * u;
+      if (c < live) {
+        const float e = ex2(p.part_lse[row0 + static_cast<size_t>(c) * w.G] - mx);
+        z += e;
+        acc[0] = fmaf(e, x[u].x, acc[0]), acc[1] = fmaf(e, x[u].y, acc[1]);
+        acc[2] = fmaf(e, x[u].z, acc[2]), acc[3] = fmaf(e, x[u].w, acc[3]);
+      }
+      if (c + 16 < live)
+        x[u] = *(reinterpret_cast<const float4*>(p.part_o + (row0 + static_cast<size_t>(c + 16) * w.G) * kHeadDim) + lane);
+    }
   }
   *(reinterpret_cast<float4*>(red[warp]) + lane) = make_float4(acc[0], acc[1], acc[2], acc[3]);
   if (lane == 0) zs[warp] = z;

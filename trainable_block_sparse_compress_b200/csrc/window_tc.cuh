@@ -574,17 +574,24 @@ __global__ void __launch_bounds__(256) window_merge_kernel(const WinTcParams p) 
   const int bg = b * w.Hkv + (h >> p.g_log2);
   const size_t cta = (static_cast<size_t>(p.row_tiles - 1 - tile) * w.B * w.Hkv + bg) * p.n_splits;
   const size_t in = static_cast<size_t>(r - tile * ct) * w.G + (h & (w.G - 1));  // row of the CTA
-  float mx = -INFINITY;
-  for (int s = 0; s < p.n_splits; ++s) mx = fmaxf(mx, p.part_lse[(cta + s) * p.rows + in]);
-  float acc[4] = {0.f, 0.f, 0.f, 0.f}, z = 0.f;
+  // lane = split (at most 32): every weight is known before the first row is read, so the reads
+  // do not wait for one another
+  const float l = lane < p.n_splits ? p.part_lse[(cta + lane) * p.rows + in] : -INFINITY;
+  float mx = l;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+  const float e = ex2(l - mx);  // 0 for a split without a visible key: its row is not read
+  float z = e;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
   for (int s = 0; s < p.n_splits; ++s) {
-    const float l = p.part_lse[(cta + s) * p.rows + in];
-    if (l == -INFINITY) continue;
-    const float e = ex2(l - mx);
-    const float4 o = *(reinterpret_cast<const float4*>(p.part_o + ((cta + s) * p.rows + in) * kHeadDim) + lane);
-    z += e;
-    acc[0] = fmaf(e, o.x, acc[0]), acc[1] = fmaf(e, o.y, acc[1]);
-    acc[2] = fmaf(e, o.z, acc[2]), acc[3] = fmaf(e, o.w, acc[3]);
+    const float es = __shfl_sync(0xffffffffu, e, s);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (es > 0.f) o = *(reinterpret_cast<const float4*>(p.part_o + ((cta + s) * p.rows + in) * kHeadDim) + lane);
+    acc[0] = fmaf(es, o.x, acc[0]), acc[1] = fmaf(es, o.y, acc[1]);
+    acc[2] = fmaf(es, o.z, acc[2]), acc[3] = fmaf(es, o.w, acc[3]);
   }
   const float inv = 1.f / z;
 #pragma unroll
