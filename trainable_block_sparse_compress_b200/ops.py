@@ -66,6 +66,20 @@ def workspace_size(p: Params, op: int, L: int) -> int:
     return v
 
 
+def _workspace_bytes(p: Params, op: int, L: int) -> int:
+    """workspace_size, remembered per problem (a function of the sizes and the device alone)."""
+    sizes = p.__dict__.get("_ws")
+    if sizes is None:
+        sizes = p.__dict__["_ws"] = {}
+    key = (op, L, _current_device())
+    n = sizes.get(key)
+    if n is None:
+        if len(sizes) >= 256:
+            sizes.clear()
+        n = sizes[key] = workspace_size(p, op, L)
+    return n
+
+
 # The binding's own time bounds the smallest calls (a decode token's GPU work is a few us), so
 # the current device and stream are read without building torch objects where torch offers it.
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
@@ -83,8 +97,8 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _need(t: torch.Tensor, name: str, dtype, shape=None):
-    if (t.is_cuda and t.dtype is dtype and t.is_contiguous() and (shape is None or t.shape == shape)
-            and t.get_device() == _current_device()):
+    # (a host tensor's get_device() is -1: it ends the comparison before a device is asked for)
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and 0 <= t.get_device() == _current_device():
         return
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -100,7 +114,7 @@ def _need(t: torch.Tensor, name: str, dtype, shape=None):
 
 
 def _workspace(p: Params, op: int, L: int, ws: Optional[torch.Tensor], like: torch.Tensor) -> Optional[torch.Tensor]:
-    n = workspace_size(p, op, L)
+    n = _workspace_bytes(p, op, L)
     if n == 0:
         return ws
     if ws is None or ws.numel() * ws.element_size() < n:
@@ -337,21 +351,17 @@ def rope_table(p: Params, inv_freq: torch.Tensor, n: int, scale: float = 1.0,
 def _need_tokens(t: torch.Tensor, name: str, B: int, L: int, H: int, d: int) -> int:
     """Token rows [B, L, H, d] with contiguous [H, d] and one stride between consecutive tokens
     (a slice of a packed projection output is such a view).  Returns that stride."""
-    if t.dim() != 4:
-        raise ValueError(f"{name} must have 4 dimensions, got {t.dim()}")
-    if tuple(t.shape) != (B, L, H, d):
+    if t.shape != (B, L, H, d):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(B, L, H, d)}")
     sb, sl, sh, sd = t.stride()
-    # device and dtype, and each token's heads contiguous (a stride over an axis of length 1 says nothing)
-    if not (t.is_cuda and t.dtype is torch.bfloat16 and sd == 1 and (sh == d or H == 1)
-            and t.get_device() == _current_device()):
-        _need(t[:1, :1], name, torch.bfloat16)
+    # a stride over an axis of length 1 says nothing
+    if not (t.dtype is torch.bfloat16 and sd == 1 and (sh == d or H == 1)
+            and 0 <= t.get_device() == _current_device()):
+        _need(t[:1, :1], name, torch.bfloat16)  # the heads of a token, as any other tensor
     if L > 1:
         stride = sl
-    elif B > 1:
-        stride = sb
     else:
-        stride = H * d
+        stride = sb if B > 1 else H * d
     if B > 1 and sb != L * stride:
         raise ValueError(f"{name} must have one stride between consecutive tokens, got {t.stride()}")
     return stride
@@ -392,12 +402,15 @@ def qk_norm_rope(p: Params, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, t
     qs = _need_tokens(q, "q", p.batch, Lq, p.num_q_heads, p.head_dim)
     ks = _need_tokens(k, "k", p.batch, Lq, p.num_kv_heads, p.head_dim)
     vs = _need_tokens(v, "v", p.batch, Lq, p.num_kv_heads, p.head_dim)
-    _need(table, "table", torch.float32)
     n, rot = table.shape
+    _need(table, "table", torch.float32, (n, rot))
     wf = _norm_weights(p, q_weight, k_weight)
-    for t, name in ((starts, "starts"), (q_lens, "q_lens"), (lens_out, "lens_out")):
-        if t is not None:
-            _need(t, name, torch.int32, (p.batch,))
+    if starts is not None:
+        _need(starts, "starts", torch.int32, (B,))
+    if q_lens is not None:
+        _need(q_lens, "q_lens", torch.int32, (B,))
+    if lens_out is not None:
+        _need(lens_out, "lens_out", torch.int32, (B,))
     if (k_cache is None) != (v_cache is None):
         raise ValueError("k_cache and v_cache go together")
     # outputs made here need no checks
@@ -414,12 +427,14 @@ def qk_norm_rope(p: Params, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, t
         k_out, v_out = k_cache, v_cache
     else:
         Lout = Lq
-        for t, name in ((k_out, "k_out"), (v_out, "v_out")):
-            if t is not None:
-                _need(t, name, torch.bfloat16, (B, p.num_kv_heads, Lq, p.head_dim))
-        if k_out is None:
-            k_out = q.new_empty((B, p.num_kv_heads, Lq, p.head_dim))
-        if v_out is None:
+        kv_shape = (B, p.num_kv_heads, Lq, p.head_dim)
+        if k_out is not None:
+            _need(k_out, "k_out", torch.bfloat16, kv_shape)
+        else:
+            k_out = q.new_empty(kv_shape)
+        if v_out is not None:
+            _need(v_out, "v_out", torch.bfloat16, kv_shape)
+        else:
             v_out = torch.empty_like(k_out)
     st = _lib.load().infllmv2_qk_norm_rope(ctypes.byref(p.c()), _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, Lq,
                                            _ptr(q_weight), _ptr(k_weight), wf, eps, _ptr(table), n, rot,
@@ -481,11 +496,13 @@ def window_attn_chunk(p: Params, q: torch.Tensor, k: torch.Tensor, v: torch.Tens
     B, Lq, Hq, d = q.shape
     Lmax = k.shape[2]
     _need(q, "q", torch.bfloat16, (p.batch, Lq, p.num_q_heads, p.head_dim))
-    _need(k, "k", torch.bfloat16, (p.batch, p.num_kv_heads, Lmax, p.head_dim))
-    _need(v, "v", torch.bfloat16, (p.batch, p.num_kv_heads, Lmax, p.head_dim))
-    for t, name in ((q_lens, "q_lens"), (kv_lens, "kv_lens")):
-        if t is not None:
-            _need(t, name, torch.int32, (p.batch,))
+    kv_shape = (p.batch, p.num_kv_heads, Lmax, p.head_dim)
+    _need(k, "k", torch.bfloat16, kv_shape)
+    _need(v, "v", torch.bfloat16, kv_shape)
+    if q_lens is not None:
+        _need(q_lens, "q_lens", torch.int32, (p.batch,))
+    if kv_lens is not None:
+        _need(kv_lens, "kv_lens", torch.int32, (p.batch,))
     if out is None:
         out = torch.empty_like(q)
     else:
@@ -524,8 +541,9 @@ def window_attn_decode(p: Params, q: torch.Tensor, k_cache: torch.Tensor, v_cach
     empty sequence)."""
     Lmax = k_cache.shape[2]
     _need(q, "q", torch.bfloat16, (p.batch, p.num_q_heads, p.head_dim))
-    _need(k_cache, "k_cache", torch.bfloat16, (p.batch, p.num_kv_heads, Lmax, p.head_dim))
-    _need(v_cache, "v_cache", torch.bfloat16, (p.batch, p.num_kv_heads, Lmax, p.head_dim))
+    kv_shape = (p.batch, p.num_kv_heads, Lmax, p.head_dim)
+    _need(k_cache, "k_cache", torch.bfloat16, kv_shape)
+    _need(v_cache, "v_cache", torch.bfloat16, kv_shape)
     _need(lens, "lens", torch.int32, (p.batch,))
     if out is None:
         out = torch.empty_like(q)
