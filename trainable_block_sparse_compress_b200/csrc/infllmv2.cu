@@ -367,7 +367,9 @@ WindowPlan window_plan(const infllmv2_params* p, int32_t Lq, long long key_tiles
   return d;
 }
 
-// Chunks of the window decode.  While every (sequence, kv-head)'s segments make no more than 8
+// Chunks of the window decode.  Up to 8 segments are one chunk: the second launch and the join cost
+// as much as the segments (8.2 us either way at 8 segments, 10.3 against 8.2 with 64 items, and 2 us
+// more host time).  Beyond that, while every (sequence, kv-head)'s segments make no more than 8
 // per CTA slot (two CTAs an SM), one wave takes them, at least two a chunk; beyond that about six
 // waves of chunks even out ragged lengths.  Counted for full caches of Lmax tokens.
 struct WindowDecodePlan {
@@ -378,6 +380,7 @@ WindowDecodePlan window_decode_plan(const infllmv2_params* p, int32_t Lmax, int3
   const long long win = (std::min<long long>(window, Lmax) + kWfSeg - 1) / kWfSeg;
   // two runs of keys may make one segment more than one run of the whole cache
   const long long segs = std::min<long long>(num_blocks(Lmax) + 1, win + (std::min<long long>(n_sink, Lmax) + kWfSeg - 1) / kWfSeg);
+  if (segs <= 8) return {8, 1};
   const long long each = (items * segs + slots - 1) / slots;
   const long long per = each <= 8 ? std::max<long long>(2, each) : std::max<long long>(8, (each + 5) / 6);
   return {static_cast<int>(per), static_cast<int>((segs + per - 1) / per)};
