@@ -459,20 +459,23 @@ def qk_norm_rope_backward(p: Params, q: torch.Tensor, k: torch.Tensor, d_q: torc
     qs = _need_tokens(q, "q", p.batch, Lq, Hq, d)
     ks = _need_tokens(k, "k", p.batch, Lq, Hkv, d)
     _need(d_q, "d_q", torch.bfloat16, (B, Lq, Hq, d))
-    _need(d_k, "d_k", torch.bfloat16, (B, Hkv, Lq, d))
-    _need(d_v, "d_v", torch.bfloat16, (B, Hkv, Lq, d))
-    _need(table, "table", torch.float32)
+    kv_shape = (B, Hkv, Lq, d)
+    _need(d_k, "d_k", torch.bfloat16, kv_shape)
+    _need(d_v, "d_v", torch.bfloat16, kv_shape)
     n, rot = table.shape
+    _need(table, "table", torch.float32, (n, rot))
     wf = _norm_weights(p, q_weight, k_weight)
-    for t, name in ((starts, "starts"), (q_lens, "q_lens")):
-        if t is not None:
-            _need(t, name, torch.int32, (p.batch,))
+    if starts is not None:
+        _need(starts, "starts", torch.int32, (B,))
+    if q_lens is not None:
+        _need(q_lens, "q_lens", torch.int32, (B,))
     if out is None:
-        out = torch.empty((B, Lq, Hq + 2 * Hkv, d), dtype=torch.bfloat16, device=q.device)
-    _need(out, "out", torch.bfloat16, (B, Lq, Hq + 2 * Hkv, d))
-    dq, dk, dv = out[:, :, :Hq], out[:, :, Hq:Hq + Hkv], out[:, :, Hq + Hkv:]
-    d_qw = None if q_weight is None else torch.empty(d, dtype=torch.float32, device=q.device)
-    d_kw = None if k_weight is None else torch.empty(d, dtype=torch.float32, device=q.device)
+        out = q.new_empty((B, Lq, Hq + 2 * Hkv, d))
+    else:
+        _need(out, "out", torch.bfloat16, (B, Lq, Hq + 2 * Hkv, d))
+    dq, dk, dv = out.split((Hq, Hkv, Hkv), 2)
+    d_qw = None if q_weight is None else q.new_empty(d, dtype=torch.float32)
+    d_kw = None if k_weight is None else q.new_empty(d, dtype=torch.float32)
     ws = _workspace(p, _lib.OP_QK_NORM_ROPE_BACKWARD, Lq, ws, q)
     nbytes = ws.numel() * ws.element_size()
     rs = (Hq + 2 * Hkv) * d
