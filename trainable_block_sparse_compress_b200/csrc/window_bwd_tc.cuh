@@ -69,6 +69,9 @@ __global__ void __launch_bounds__(256) window_delta_kernel(const WinBwdParams p)
     const int h0 = static_cast<int>(it - tok * groups) * 4, t = static_cast<int>(tok - b * p.Lp);
     const bool in = t < chunk_lens(w.q_lens, w.kv_lens, static_cast<int>(b), w.Lq, w.Lmax).q_len;
     const size_t o = ((static_cast<size_t>(b) * w.Lq + t) * w.Hq + h0) * kHeadDim;
+    const bool mine = l < 4 && h0 + l < w.Hq;  // lane l: head h0 + l
+    float lse = INFINITY, dl = 0.f;
+    if (in && mine) lse = w.lse[(static_cast<size_t>(b) * w.Hq + h0 + l) * w.Lq + t] * 1.4426950408889634f;
     uint4 x[4], y[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -89,12 +92,13 @@ __global__ void __launch_bounds__(256) window_delta_kernel(const WinBwdParams p)
       }
 #pragma unroll
       for (int d = 8; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d, 16);
-      const int h = h0 + u;
-      if (l == 0 && h < w.Hq) {
-        const size_t i = ((static_cast<size_t>(b) * w.Hkv + (h >> p.g_log2)) * p.Lp + t) * w.G + (h & (w.G - 1));
-        p.lse2[i] = in ? w.lse[(static_cast<size_t>(b) * w.Hq + h) * w.Lq + t] * -1.4426950408889634f : -INFINITY;
-        p.delta[i] = -s;
-      }
+      if (l == u) dl = s;
+    }
+    if (mine) {
+      const int h = h0 + l;
+      const size_t i = ((static_cast<size_t>(b) * w.Hkv + (h >> p.g_log2)) * p.Lp + t) * w.G + (h & (w.G - 1));
+      p.lse2[i] = -lse;
+      p.delta[i] = -dl;
     }
   }
 }
