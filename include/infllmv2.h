@@ -412,7 +412,9 @@ INFLLMV2_API int infllmv2_qk_norm_rope_backward(
  *   window     >= 1;  n_sink >= 0
  *   o          bf16 [B, Lq, Hq, d];  lse fp32 [B, Hq, Lq] or NULL
  *   ws         at least infllmv2_workspace_size(p, INFLLMV2_OP_WINDOW_ATTN, Lq) bytes (may be
- *              NULL when that size is 0); contents on entry do not matter
+ *              NULL when that size is 0); contents on entry do not matter.  Calls that overlap
+ *              on the GPU need a workspace each.
+ * UNSUPPORTED past 2^31 - 1 query rows (B Lq Hq) or cache rows (B Hkv Lmax).
  * Padding rows (r >= q_lens[b]) are not written.  Cache rows that no query of the call sees
  * may hold anything, NaN included; a key or value row that some query sees must be finite
  * (an infinity or NaN there may reach other queries of the call that do not see it). */
@@ -442,8 +444,9 @@ INFLLMV2_API int infllmv2_window_attn_decode(const infllmv2_params* p, const voi
  *              rows at or past lens[b] are padding: not read, and their gradients not written
  *   dq         bf16 [B, L, Hq, d];  dk, dv bf16 [B, Hkv, L, d] (outputs)
  *   ws         at least infllmv2_workspace_size(p, INFLLMV2_OP_WINDOW_BACKWARD, L) bytes
- * Deterministic: no atomics; a shared head's dk and dv are summed over its group inside one
- * CTA. */
+ *              (contents on entry do not matter; calls that overlap on the GPU need one each)
+ * Deterministic: no atomics, every sum in a fixed order.  UNSUPPORTED past 65535 (sequence,
+ * kv-head)s. */
 INFLLMV2_API int infllmv2_window_attn_backward(const infllmv2_params* p, const void* q, const void* k, const void* v,
                                                const void* o, const float* lse, const void* d_o, const int32_t* lens,
                                                int32_t L, int32_t window, int32_t n_sink, void* dq, void* dk, void* dv,

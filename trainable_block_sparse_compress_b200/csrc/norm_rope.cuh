@@ -19,7 +19,7 @@
 // Measured on a 128K prompt, 32 / 2 heads, 2.48 GB: 412 us (0.92 of the measured copy bandwidth);
 // 12 heads an item 442, six rows in flight at two CTAs an SM 526, one wave of CTAs (the short key
 // and value items then leave their SMs early) 477 to 806.  Backward, 2 x 8191 tokens, 449 MB:
-// 111 us (0.61); two rows in flight at three CTAs an SM 121.
+// 105 us (0.65); two rows in flight at three CTAs an SM 121, eight rows at two 113.
 #pragma once
 #include "append.cuh"
 #include "common.cuh"

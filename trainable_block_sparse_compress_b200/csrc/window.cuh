@@ -26,4 +26,5 @@ struct WinParams {
 __device__ __forceinline__ void store4(__nv_bfloat16* p, int lane, const float (&x)[4]) {
   *(reinterpret_cast<uint2*>(p) + lane) = make_uint2(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]));
 }
+
 }  // namespace infllmv2

@@ -10,6 +10,8 @@
 // with its own reference per warp, and P V, with no synchronisation between the warps until the
 // chunk ends.  Chunks are joined by window_decode_merge_kernel through the workspace; a
 // (sequence, kv-head) that is one chunk writes its output directly.
+// Measured: 32 ragged 128K sequences, 32 / 2 heads, every key: 452 us, 7.1 TB/s; 8 sequences, W 4096:
+// 14 us, of which the two launches, the lengths and the join are about 9.
 #pragma once
 #include "common.cuh"
 #include "tcgen05.cuh"
