@@ -234,7 +234,9 @@ int launch_pdl(void (*kern)(Params...), dim3 grid, int threads, size_t smem, cud
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...) == cudaSuccess ? INFLLMV2_OK : INFLLMV2_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...) == cudaSuccess) return INFLLMV2_OK;
+  (void)cudaGetLastError();  // reported here, not by the next call
+  return INFLLMV2_ERR_CUDA;
 }
 
 // Decode work layout.  Each (sequence, kv-head) item's selected blocks are split over
