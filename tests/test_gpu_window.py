@@ -187,6 +187,23 @@ def test_decode_matches_reference_and_ignores_what_it_does_not_see(Lmax, Hq, Hkv
     assert torch.equal(o, o2)
 
 
+# from one chunk to a cluster of 16 and past it, with sequences that end in its first and last chunks
+@pytest.mark.parametrize("Lmax", [512, 513, 640, 1024, 2047, 3008, 3200])
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (16, 1), (6, 3)])
+def test_decode_joins_its_chunks(Lmax, Hq, Hkv):
+    lens = [Lmax, 1, Lmax - 1, 129]
+    q, k, v = inputs(len(lens), 1, Lmax, Hq, Hkv, seed=Lmax)
+    p = ops.Params(len(lens), Hq, Hkv)
+    lt = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    o, lse = ops.window_attn_decode(p, q[:, 0], k, v, lt, Lmax, 0)
+    check_rows(o[:, None], lse[..., None], q, k, v, [1] * len(lens), lens, Lmax, 0, "decode")
+    v[0, 0, Lmax - 1, 5] = NAN  # seen by sequence 0 alone, and by column 5 of its first group
+    o2, lse2 = ops.window_attn_decode(p, q[:, 0], k, v, lt, Lmax, 0)
+    nan = torch.zeros_like(o, dtype=torch.bool)
+    nan[0, :Hq // Hkv, 5] = True
+    assert torch.equal(o2.isnan(), nan) and torch.equal(lse, lse2) and torch.equal(o2[~nan], o[~nan])
+
+
 def test_decode_empty_and_overlong_sequences():
     q, k, v = inputs(4, 1, 200, 8, 2, seed=2)
     lt = torch.tensor([0, -3, 1000, 5], dtype=torch.int32, device="cuda")

@@ -369,24 +369,34 @@ WindowPlan window_plan(const infllmv2_params* p, int32_t Lq, long long key_tiles
   return d;
 }
 
-// Chunks of the window decode.  Up to 8 segments are one chunk: the second launch and the join cost
-// as much as the segments (8.2 us either way at 8 segments, 10.3 against 8.2 with 64 items, and 2 us
-// more host time).  Beyond that, while every (sequence, kv-head)'s segments make no more than 8
-// per CTA slot (two CTAs an SM), one wave takes them, at least two a chunk; beyond that about six
-// waves of chunks even out ragged lengths.  Counted for full caches of Lmax tokens.
+// Chunks of the window decode.  Up to 8 segments are one chunk: the join costs as much as the
+// segments (8.2 us either way at 8 segments, 10.3 against 8.2 with 64 items, and 2 us more host
+// time).  Beyond that, while every (sequence, kv-head)'s segments make no more than 8 per CTA slot
+// (two CTAs an SM), one wave takes them, at least two a chunk; beyond that about six waves of chunks
+// even out ragged lengths.  Chunks that a cluster of 16 could take with at most half as many again
+// are one, while the device holds every item's cluster at once.  Counted for full caches of Lmax
+// tokens.
 struct WindowDecodePlan {
   int per_chunk, chunks;
+  bool cluster;
 };
 WindowDecodePlan window_decode_plan(const infllmv2_params* p, int32_t Lmax, int32_t window, int32_t n_sink) {
   const long long items = static_cast<long long>(p->batch) * p->num_kv_heads, slots = 2LL * num_sms();
   const long long win = (std::min<long long>(window, Lmax) + kWfSeg - 1) / kWfSeg;
   // two runs of keys may make one segment more than one run of the whole cache
   const long long segs = std::min<long long>(num_blocks(Lmax) + 1, win + (std::min<long long>(n_sink, Lmax) + kWfSeg - 1) / kWfSeg);
-  if (segs <= 8) return {8, 1};
+  if (segs <= 8) return {8, 1, false};
   const long long each = (items * segs + slots - 1) / slots;
   const long long per = each <= 8 ? std::max<long long>(2, each) : std::max<long long>(8, (each + 5) / 6);
-  return {static_cast<int>(per), static_cast<int>((segs + per - 1) / per)};
+  const long long per_c = std::max(per, (segs + kWdMaxCluster - 1) / kWdMaxCluster);
+  if (2 * per_c <= 3 * per) {
+    const int chunks = static_cast<int>((segs + per_c - 1) / per_c);
+    if (items <= max_active_clusters(window_decode_kernel<true>, chunks, kWdThreads, window_decode_smem_bytes()))
+      return {static_cast<int>(per_c), chunks, true};
+  }
+  return {static_cast<int>(per), static_cast<int>((segs + per - 1) / per), false};
 }
+
 // Backward of the window attention: cuts of the key tiles' query ranges (counted for sequences
 // of L tokens).  The aim is two CTAs of equal work an SM, at least 16 query tiles each (a partial
 // costs a write and a read of 128 KB): a kind of key tile whose range is n such shares, rounded,
@@ -722,9 +732,12 @@ int launch_window_decode(const infllmv2_params* p, const WinParams& w, void* ws,
       !sink_maps(w, tk, tv, &tks, &tvs))
     return INFLLMV2_ERR_CUDA;
   const size_t smem = window_decode_smem_bytes();
-  int st = set_smem(reinterpret_cast<const void*>(window_decode_kernel), smem);
+  const unsigned grid = static_cast<unsigned>(items * d.chunks);
+  if (d.cluster)
+    return launch_cluster(window_decode_kernel<true>, grid, d.chunks, kWdThreads, smem, s, true, tk, tv, tks, tvs, a);
+  int st = set_smem(reinterpret_cast<const void*>(window_decode_kernel<false>), smem);
   if (st != INFLLMV2_OK) return st;
-  st = launch_pdl(window_decode_kernel, static_cast<unsigned>(items * d.chunks), kWdThreads, smem, s, tk, tv, tks, tvs, a);
+  st = launch_pdl(window_decode_kernel<false>, grid, kWdThreads, smem, s, tk, tv, tks, tvs, a);
   if (st != INFLLMV2_OK || d.chunks == 1) return st;
   return launch_pdl(window_decode_merge_kernel, static_cast<unsigned>(w.B * w.Hq), 128, 0, s, a);
 }

@@ -8,11 +8,14 @@
 // CTAs share an SM and keep 192 KB in flight); warps 0-3 take 16 keys of each segment: 16 heads
 // x 16 keys of scores with m16n8k16 MMAs (a tcgen05 tile would need 64 rows), an online softmax
 // with its own reference per warp, and P V, with no synchronisation between the warps until the
-// chunk ends.  Chunks are joined by window_decode_merge_kernel through the workspace; a
-// (sequence, kv-head) that is one chunk writes its output directly.
+// chunk ends.  A (sequence, kv-head) that is one chunk writes its output directly; up to 16 chunks
+// are a thread-block cluster and joined through distributed shared memory (one launch, no round
+// trip through HBM); more are joined by window_decode_merge_kernel through the workspace.
 // Measured: 32 ragged 128K sequences, 32 / 2 heads, every key: 452 us, 7.1 TB/s; 8 sequences, W 4096:
-// 14 us, of which the two launches, the lengths and the join are about 9.
+// 12.3 us in one cluster launch, 13.1 us with the join through the workspace (cold L2: 20.5, 21.5).
 #pragma once
+#include <cooperative_groups.h>
+
 #include "common.cuh"
 #include "tcgen05.cuh"
 #include "window_tc.cuh"
@@ -28,12 +31,15 @@ constexpr int kWdStageBytes = 4 * kWdHalf;     // K halves, then V halves
 struct WdSmem {
   uint64_t full[kWdStages], empty[kWdStages];
   float m[kWdWarps][kGroupRows], l[kWdWarps][kGroupRows];
+  float lse[kGroupRows];  // cluster: this CTA's base-2 log-sum-exps
   volatile int abort;
 };
 constexpr size_t window_decode_smem_bytes() {
   return 1024 + static_cast<size_t>(kWdStages) * kWdStageBytes + sizeof(WdSmem);
 }
-static_assert(kWdStages * kWdStageBytes >= kWdWarps * kGroupRows * kHeadDim * 4, "the warps' partial outputs");
+constexpr int kWdPartFloats = kWdWarps * kGroupRows * kHeadDim;  // the warps' partial outputs, then the CTA's
+static_assert(kWdStages * kWdStageBytes >= (kWdPartFloats + kGroupRows * kHeadDim) * 4, "partial outputs in the ring");
+constexpr int kWdMaxCluster = 16;
 
 struct WinDecodeParams {
   WinParams w;
@@ -42,7 +48,9 @@ struct WinDecodeParams {
   float* part_lse;                // [B * Hkv, chunks, G] base 2
 };
 
-// grid = B * Hkv * chunks; a CTA past its sequence's keys ends at once.
+// grid = B * Hkv * chunks.  A CTA past its sequence's keys ends at once, or (kCluster: the chunks of
+// a (sequence, kv-head) are one cluster) only takes part in the join.
+template <bool kCluster>
 __global__ void __launch_bounds__(kWdThreads, 2)
     window_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                          const __grid_constant__ CUtensorMap tm_ks, const __grid_constant__ CUtensorMap tm_vs,
@@ -80,8 +88,8 @@ __global__ void __launch_bounds__(kWdThreads, 2)
   const WinRuns runs(t, t, w.window, w.n_sink);
   const int segs = runs.ns + runs.nw;
   const int s0 = chunk * p.per_chunk, s1 = min(segs, s0 + p.per_chunk);
-  if (s0 >= s1) return;
-  const int n = s1 - s0;
+  if (!kCluster && s0 >= s1) return;
+  const int n = max(s1 - s0, 0);
 
   if (warp == kWdWarps) {
     if (lane == 0) {
@@ -217,8 +225,13 @@ __global__ void __launch_bounds__(kWdThreads, 2)
               make_float2(o[d][2 * h], o[d][2 * h + 1]);
   __syncthreads();
   // join the warps: a thread takes 4 columns of rows threadIdx / 32, + 4, ...
+  float* joint = part + kWdPartFloats;  // cluster: [row][128]
   if (warp < kWdWarps)
     for (int row = warp; row < w.G; row += kWdWarps) {
+      if (kCluster && n == 0) {
+        if (lane == 0) S.lse[row] = -INFINITY;
+        continue;
+      }
       float mm = -INFINITY;
 #pragma unroll
       for (int v = 0; v < kWdWarps; ++v) mm = fmaxf(mm, S.m[v][row]);
@@ -235,7 +248,10 @@ __global__ void __launch_bounds__(kWdThreads, 2)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[i] *= inv;
       const size_t head = static_cast<size_t>(b) * w.Hq + (g << p.g_log2) + row;
-      if (p.chunks == 1) {
+      if (kCluster) {
+        *(reinterpret_cast<float4*>(joint + row * kHeadDim) + lane) = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        if (lane == 0) S.lse[row] = lse2;
+      } else if (p.chunks == 1) {
         store4(w.o + head * kHeadDim, lane, acc);
         if (w.lse && lane == 0) w.lse[head] = lse2 * 0.6931471805599453f;
       } else {
@@ -244,6 +260,39 @@ __global__ void __launch_bounds__(kWdThreads, 2)
         if (lane == 0) p.part_lse[pr] = lse2;
       }
     }
+  if (kCluster) {
+    namespace cg = cooperative_groups;
+    cg::cluster_group cluster = cg::this_cluster();
+    cluster.sync();  // every CTA's rows are final
+    if (warp < kWdWarps)
+      for (int row = chunk * kWdWarps + warp; row < w.G; row += p.chunks * kWdWarps) {
+        // lane = chunk (at most 16): every weight is known before the first row is read
+        const float l = lane < p.chunks ? cluster.map_shared_rank(S.lse, lane)[row] : -INFINITY;
+        float mx = l;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+        const float e = ex2(l - mx);  // 0 for a chunk without keys: its row is not read
+        float z = e;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int c = 0; c < p.chunks; ++c) {
+          const float ec = __shfl_sync(0xffffffffu, e, c);
+          float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (ec > 0.f) x = *(reinterpret_cast<const float4*>(cluster.map_shared_rank(joint, c) + row * kHeadDim) + lane);
+          acc[0] = fmaf(ec, x.x, acc[0]), acc[1] = fmaf(ec, x.y, acc[1]);
+          acc[2] = fmaf(ec, x.z, acc[2]), acc[3] = fmaf(ec, x.w, acc[3]);
+        }
+        const float inv = 1.f / z;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] *= inv;
+        const size_t head = static_cast<size_t>(b) * w.Hq + (g << p.g_log2) + row;
+        store4(w.o + head * kHeadDim, lane, acc);
+        if (w.lse && lane == 0) w.lse[head] = (mx + lg2(z)) * 0.6931471805599453f;
+      }
+    cluster.sync();  // the others' shared memory stays until every row has been read
+  }
 }
 
 // Joins the chunks: a CTA per (sequence, q-head), its four warps taking every fourth chunk.
