@@ -188,6 +188,36 @@ def test_zero_rows_and_backward_padding():
     close(r[3], dw, tw, "d_qw")
 
 
+# several chunks of query and of key and value heads, with ragged ends, padding and an empty sequence
+@pytest.mark.parametrize("L,Hq,Hkv", [(1201, 10, 10), (900, 16, 16), (2050, 5, 5), (1400, 36, 9), (701, 14, 7)])
+def test_backward_over_chunks_of_heads(L, Hq, Hkv):
+    p = ops.Params(3, Hq, Hkv)
+    q, k, v = projection(3, L, Hq, Hkv, seed=L)
+    n, t0 = [L, L - 77, 0], [0, 40, 3]
+    for b in range(3):
+        q[b, n[b]:], k[b, n[b]:] = NAN, NAN
+    qw, kw = weights("fp32", L)
+    table = ops.rope_table(p, inv_freq(96), L)
+    g = torch.Generator(device="cuda").manual_seed(L)
+    dq, dk, dv = (randn(g, *x) for x in ((3, L, Hq, 128), (3, Hkv, L, 128), (3, Hkv, L, 128)))
+    out = torch.full((3, L, Hq + 2 * Hkv, 128), 7., dtype=BF, device="cuda")
+    r = ops.qk_norm_rope_backward(p, q, k, dq, dk, dv, table, qw, kw, starts=i32(*t0), q_lens=i32(*n), out=out)
+    want = {3: [0., 0.], 4: [0., 0.]}
+    for b in range(2):
+        m, tab = n[b], table[t0[b]:t0[b] + n[b]]
+        for i, x, w, d in ((0, q, qw, dq[b, :m]), (1, k, kw, dk[b, :, :m].transpose(0, 1))):
+            dx, tol, dw, tw = norm_rope_backward(x[b, :m], w, 1e-6, tab, False, d)
+            close(r[i][b, :m], dx, tol, "dx")
+            want[3 + i] = [want[3 + i][0] + dw, want[3 + i][1] + tw]
+        assert torch.equal(r[2][b, :m], dv[b, :, :m].transpose(0, 1))
+        assert (out[b, m:] == 7).all()
+    assert (out[2] == 7).all()
+    for i in (3, 4):
+        close(r[i], *want[i], "dw")
+    r2 = ops.qk_norm_rope_backward(p, q, k, dq, dk, dv, table, qw, kw, starts=i32(*t0), q_lens=i32(*n))
+    assert torch.equal(r[3], r2[3]) and torch.equal(r[4], r2[4])
+
+
 def test_backward_against_differences():
     p = ops.Params(1, 2, 1)
     q, k, v = projection(1, 9, 2, 1, seed=14)

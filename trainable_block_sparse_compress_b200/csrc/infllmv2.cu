@@ -441,10 +441,9 @@ WindowBwdPlan window_bwd_plan(const infllmv2_params* p, int32_t L, int32_t windo
   return d;
 }
 
-unsigned norm_rope_grid(const infllmv2_params* p, int32_t Lq, int ctas_per_sm, int rounds, NormRopeParams* a);
-// CTAs per SM and waves of the norm-and-rotation kernels (the backward's CTAs leave a row of
-// partial weight gradients each).
-constexpr int kNrCtas = 4, kNrWaves = 32, kNrBwdCtas = 2, kNrBwdWaves = 2;
+unsigned norm_rope_bwd_grid(const infllmv2_params* p, int32_t Lq, NormRopeParams* a);
+// CTAs per SM of the norm-and-rotation kernels, and waves of the forward.
+constexpr int kNrCtas = 4, kNrWaves = 32;
 
 size_t ws_size(const infllmv2_params* p, int op, int32_t L) {
   if (check_params(p) != INFLLMV2_OK || check_len(L) != INFLLMV2_OK) return static_cast<size_t>(-1);
@@ -465,7 +464,7 @@ size_t ws_size(const infllmv2_params* p, int op, int32_t L) {
     }
     case INFLLMV2_OP_QK_NORM_ROPE_BACKWARD: {
       NormRopeParams a;
-      return static_cast<size_t>(norm_rope_grid(p, L, kNrBwdCtas, kNrBwdWaves, &a)) * kHeadDim * sizeof(float);
+      return static_cast<size_t>(norm_rope_bwd_grid(p, L, &a)) * kHeadDim * sizeof(float);
     }
     case INFLLMV2_OP_WINDOW_ATTN: {
       const WindowPlan d = window_plan(p, L, 1 << 30);  // for every window
@@ -530,10 +529,10 @@ int norm_rope_args(const infllmv2_params* p, const void* q, int64_t q_stride, co
   return INFLLMV2_OK;
 }
 
-// Heads of one chunk and the launch's grid (0: too large): up to 8 heads a half-warp (the table
-// row and the weights are loaded once for them), fewer while the launch would leave half of the
-// GPU's warps (ctas_per_sm CTAs an SM) without work.  `rounds` bounds the CTAs at that many waves.
-unsigned norm_rope_grid(const infllmv2_params* p, int32_t Lq, int ctas_per_sm, int rounds, NormRopeParams* a) {
+// Heads of one chunk: up to 8 heads a half-warp (the table row and the weights are loaded once for
+// them), fewer while the launch would leave half of the GPU's warps (ctas_per_sm CTAs an SM)
+// without work.  Returns the token pairs.
+long long norm_rope_chunks(const infllmv2_params* p, int32_t Lq, int ctas_per_sm, NormRopeParams* a) {
   const long long pairs = (static_cast<long long>(p->batch) * Lq + 1) / 2;
   const long long room = static_cast<long long>(ctas_per_sm) * num_sms();
   const int Hq = p->num_q_heads, H2 = 2 * p->num_kv_heads;
@@ -544,9 +543,30 @@ unsigned norm_rope_grid(const infllmv2_params* p, int32_t Lq, int ctas_per_sm, i
   a->heads = heads == 1 ? 1 : std::max((Hq + qc - 1) / qc, std::min(heads, H2));
   a->q_chunks = (Hq + a->heads - 1) / a->heads;
   a->kv_chunks = (H2 + a->heads - 1) / a->heads;
-  const long long chunks = a->q_chunks + a->kv_chunks;
-  const long long x = std::min<long long>((pairs + kNrWarps - 1) / kNrWarps, std::max<long long>(1, rounds * room / chunks));
+  return pairs;
+}
+
+// Grid of the forward (0: too large): as many CTAs for every chunk, at most kNrWaves waves.
+unsigned norm_rope_grid(const infllmv2_params* p, int32_t Lq, NormRopeParams* a) {
+  const long long pairs = norm_rope_chunks(p, Lq, kNrCtas, a), chunks = a->q_chunks + a->kv_chunks;
+  const long long room = static_cast<long long>(kNrWaves) * kNrCtas * num_sms();
+  const long long x = std::min<long long>((pairs + kNrWarps - 1) / kNrWarps, std::max<long long>(1, room / chunks));
+  a->q_ctas = a->kv_ctas = static_cast<int>(x);
   return x * chunks > 0x7fffffffLL ? 0u : static_cast<unsigned>(x * chunks);
+}
+
+// Grid of the backward (0: too large): one wave, dealt to the chunks by the rows that they move for a
+// token (three a query or key head, two a value head).
+unsigned norm_rope_bwd_grid(const infllmv2_params* p, int32_t Lq, NormRopeParams* a) {
+  const long long most = (norm_rope_chunks(p, Lq, kNrBwdCtas, a) + kNrWarps - 1) / kNrWarps;
+  const long long room = static_cast<long long>(kNrBwdCtas) * num_sms(), qc = a->q_chunks, kc = a->kv_chunks;
+  const long long wq = 3 * a->heads, wkv = 5 * ((p->num_kv_heads + kc - 1) / kc);
+  const long long xq = std::max<long long>(1, room * wq / (qc * wq + kc * wkv));
+  const long long xkv = std::max<long long>(1, (room - qc * xq) / kc);
+  a->q_ctas = static_cast<int>(std::min(most, xq));
+  a->kv_ctas = static_cast<int>(std::min(most, xkv));
+  const long long grid = qc * a->q_ctas + kc * a->kv_ctas;
+  return grid > 0x7fffffffLL ? 0u : static_cast<unsigned>(grid);
 }
 
 // Shared checks and parameters of the window attention calls.
@@ -1275,7 +1295,7 @@ int infllmv2_qk_norm_rope(const infllmv2_params* p, const void* q, int64_t q_str
   a.Lout = Lout;
   a.at_position = at_position;
   a.lens_out = lens_out;
-  const unsigned grid = norm_rope_grid(p, Lq, kNrCtas, kNrWaves, &a);
+  const unsigned grid = norm_rope_grid(p, Lq, &a);
   if (grid == 0) return INFLLMV2_ERR_UNSUPPORTED;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return interleaved ? launch_pdl(qk_norm_rope_kernel<true>, grid, kNrThreads, 0, s, a)
@@ -1312,17 +1332,15 @@ int infllmv2_qk_norm_rope_backward(const infllmv2_params* p, const void* q, int6
   a.dk_stride = dk_stride;
   a.dv_stride = dv_stride;
   a.part = static_cast<float*>(ws);
-  const unsigned grid = norm_rope_grid(p, Lq, kNrBwdCtas, kNrBwdWaves, &a);
+  const unsigned grid = norm_rope_bwd_grid(p, Lq, &a);
   if (grid == 0) return INFLLMV2_ERR_UNSUPPORTED;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (interleaved)
-    qk_norm_rope_bwd_kernel<true><<<grid, kNrThreads, 0, s>>>(a);
-  else
-    qk_norm_rope_bwd_kernel<false><<<grid, kNrThreads, 0, s>>>(a);
+  auto kernel = interleaved ? qk_norm_rope_bwd_kernel<true> : qk_norm_rope_bwd_kernel<false>;
+  if ((st = set_smem(reinterpret_cast<const void*>(kernel), kNrBwdSmem)) != INFLLMV2_OK) return st;
+  kernel<<<grid, kNrThreads, kNrBwdSmem, s>>>(a);
   if ((st = launch_status()) != INFLLMV2_OK || (!d_qw && !d_kw)) return st;
-  const int each = static_cast<int>(grid) / (a.q_chunks + a.kv_chunks);
-  return launch_pdl(qk_norm_rope_bwd_weights_kernel, dim3(8), 1024, 0, s, a.part, a.q_chunks * each,
-                    a.kv_chunks * each, d_qw, d_kw);
+  return launch_pdl(qk_norm_rope_bwd_weights_kernel, dim3(8), 1024, 0, s, a.part, a.q_chunks * a.q_ctas,
+                    a.kv_chunks * a.kv_ctas, d_qw, d_kw);
 }
 
 int infllmv2_window_attn(const infllmv2_params* p, const void* q, int32_t Lq, const void* k, const void* v,

@@ -13,14 +13,20 @@
 // way).  A half-warp holds a row, a lane two runs of 4 values that are each other's rotation
 // partners (rot / 2 apart, or adjacent for interleaved pairs), so a rotation needs no shuffle
 // and 4 cosines and sines a lane; the norm is four shuffles.  A half-warp takes several heads
-// of one token (all queries, or keys then values), so the token's row of the table and one
+// of one token (all queries, or keys and values), so the token's row of the table and one
 // weight vector stay in registers, with kNrRows rows in flight; the arithmetic is packed in
 // pairs (f32x2), since with one value an instruction the issue slots, not HBM, would bound it.
 // Measured on a 128K prompt, 32 / 2 heads, 2.48 GB: 412 us (0.92 of the measured copy bandwidth);
 // 12 heads an item 442, six rows in flight at two CTAs an SM 526, one wave of CTAs (the short key
-// and value items then leave their SMs early) 477 to 806.  Backward, 2 x 8191 tokens, 449 MB:
-// 105 us (0.65); two rows in flight at three CTAs an SM 121, eight rows at two 113.
+// and value items then leave their SMs early) 477 to 806.
+// The backward copies a lane's values into its own slots of shared memory, kNrBwdRows rows ahead
+// of the ones it works on: rows in flight cost no registers.  One wave of CTAs, dealt to the query
+// and to the key and value heads by their bytes.  Measured, 2 x 8191 tokens, 453 MB: 92 us (0.75; 0.85
+// at 65536 tokens); rows loaded into registers 112, as many CTAs for each chunk of heads 103, two
+// rows ahead 100, eight rows with 12 warps an SM 120, one row's dependent chain at a time 94.
 #pragma once
+#include <type_traits>
+
 #include "append.cuh"
 #include "common.cuh"
 
@@ -29,7 +35,8 @@ namespace infllmv2 {
 constexpr int kNrThreads = 256;
 constexpr int kNrWarps = kNrThreads / 32;
 constexpr int kNrRows = 4;       // head rows in flight per half-warp, forward
-constexpr int kNrBwdRows = 4;    // backward (two loads a row)
+constexpr int kNrBwdRows = 4;    // backward: rows of a batch
+constexpr int kNrBwdCtas = 2;    // CTAs an SM
 
 struct NormRopeParams {
   const __nv_bfloat16 *q, *k, *v;        // token rows
@@ -41,9 +48,10 @@ struct NormRopeParams {
   int32_t* lens_out;
   const __nv_bfloat16 *dq, *dk, *dv;     // backward: gradients in the attention's layouts
   long long dq_stride, dk_stride, dv_stride;
-  float* part;                           // backward: [chunk][CTA of it][128] partial d_w
+  float* part;                           // backward: [CTA][128] partial d_w
   int B, Lq, Hq, Hkv, Lout, at_position, weights_fp32, table_rows, rot;
-  int heads, q_chunks, kv_chunks;        // heads of one chunk; grid = chunks * CTAs of a chunk
+  int heads, q_chunks, kv_chunks;        // heads of one chunk, chunks of a token
+  int q_ctas, kv_ctas;                   // CTAs of a query chunk, of a key and value chunk
   float eps;
 };
 
@@ -175,19 +183,33 @@ struct NormRopeToken {
 };
 
 // A CTA's chunk of heads (p.heads query heads, or p.heads of the Hkv key and then Hkv value heads)
-// and its place among the chunk's CTAs: the chunks of a token run side by side.
+// and its place among the chunk's CTAs.  kEven: as many CTAs for every chunk, the chunks of a
+// token side by side; else the query chunks' CTAs come first.
+template <bool kEven>
 struct NormRopeChunk {
   int chunk, h0, h1;
   unsigned x, ctas;
   bool isq;
   __device__ __forceinline__ explicit NormRopeChunk(const NormRopeParams& p) {
-    const unsigned n = p.q_chunks + p.kv_chunks;
-    chunk = static_cast<int>(blockIdx.x % n);
-    x = blockIdx.x / n;
-    ctas = gridDim.x / n;
-    isq = chunk < p.q_chunks;
+    if (kEven) {
+      const unsigned n = p.q_chunks + p.kv_chunks;
+      chunk = static_cast<int>(blockIdx.x % n);
+      x = blockIdx.x / n;
+      ctas = gridDim.x / n;
+      isq = chunk < p.q_chunks;
+    } else {
+      const unsigned i = blockIdx.x, q = p.q_chunks * p.q_ctas, kc = p.kv_chunks, qc = p.q_chunks;
+      isq = i < q;
+      chunk = static_cast<int>(isq ? i % qc : qc + (i - q) % kc);
+      x = isq ? i / qc : (i - q) / kc;
+      ctas = isq ? p.q_ctas : p.kv_ctas;
+    }
     h0 = (isq ? chunk : chunk - p.q_chunks) * p.heads;
     h1 = min(h0 + p.heads, isq ? p.Hq : 2 * p.Hkv);
+  }
+  // the CTA's row of the partial weight gradients: the query chunks', then the key and value chunks'
+  __device__ __forceinline__ int part(const NormRopeParams& p) const {
+    return static_cast<int>((isq ? chunk * ctas : p.q_chunks * p.q_ctas + (chunk - p.q_chunks) * ctas) + x);
   }
 };
 
@@ -197,7 +219,7 @@ __global__ void __launch_bounds__(kNrThreads, 4) qk_norm_rope_kernel(const NormR
   grid_dependency_wait();
   const int l = threadIdx.x & 15;
   const unsigned tokens = static_cast<unsigned>(p.B) * static_cast<unsigned>(p.Lq);
-  const NormRopeChunk ch(p);
+  const NormRopeChunk<true> ch(p);
   const bool isq = ch.isq;
   const int h0 = ch.h0, h1 = ch.h1;
   int ra, rb;
@@ -249,73 +271,160 @@ __global__ void __launch_bounds__(kNrThreads, 4) qk_norm_rope_kernel(const NormR
   }
 }
 
+// Asynchronous copy of a lane's N bytes into its own slot of shared memory; zeros unless `live`.
+template <int N>
+__device__ __forceinline__ void copy_async(void* dst, const void* src, bool live) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(src), "n"(N), "r"(live ? N : 0)
+               : "memory");
+}
+
+// A warp's buffers of the backward: the rows of two batches of heads and the angles of
+// two tokens, a lane's values in the lane's own slots (no conflicts, nothing to synchronise).
+struct NrBwdWarp {
+  uint2 x[2][kNrBwdRows][2][32], g[2][kNrBwdRows][2][32];
+  float4 cs[2][2][32];
+};
+constexpr size_t kNrBwdSmem = kNrWarps * sizeof(NrBwdWarp);
+static_assert(sizeof(NrBwdWarp) >= 2 * kHeadDim * sizeof(float), "the half-warps' weight gradients");
+
 // The backward over the same chunks: input gradients, and one row of partial weight gradients
-// per CTA (its half-warps' sums added in a fixed order).
+// per CTA (its half-warps' sums added in a fixed order).  The next batch of heads (or the next
+// token's first) is copied into shared memory while one is worked on.
 template <bool kInterleaved>
-__global__ void __launch_bounds__(kNrThreads, 2) qk_norm_rope_bwd_kernel(const NormRopeParams p) {
-  const int l = threadIdx.x & 15;
-  const unsigned tokens = static_cast<unsigned>(p.B) * static_cast<unsigned>(p.Lq);
-  const NormRopeChunk ch(p);
+__global__ void __launch_bounds__(kNrThreads, kNrBwdCtas) qk_norm_rope_bwd_kernel(const NormRopeParams p) {
+  extern __shared__ __align__(16) unsigned char nr_smem[];
+  const int l = threadIdx.x & 15, lane = threadIdx.x & 31;
+  NrBwdWarp& S = reinterpret_cast<NrBwdWarp*>(nr_smem)[threadIdx.x >> 5];
+  const unsigned tokens = static_cast<unsigned>(p.B) * static_cast<unsigned>(p.Lq), pairs = (tokens + 1) / 2;
+  const NormRopeChunk<false> ch(p);
   const bool isq = ch.isq;
-  const int h0 = ch.h0, h1 = ch.h1;
+  // the key and value heads are dealt to their chunks in turn: each chunk has its share of both
+  const int hs = isq ? 1 : p.kv_chunks, h0 = isq ? ch.h0 : ch.chunk - p.q_chunks, h1 = isq ? ch.h1 : 2 * p.Hkv;
+  const int hn = isq ? h1 : p.Hkv;  // heads with a norm
   int ra, rb;
   lane_runs<kInterleaved>(p.rot, l, ra, rb);
   const Row8 w = load_weights(isq ? p.qw : p.kw, p.weights_fp32, ra, rb);
+  const size_t head = static_cast<size_t>(p.Lq) * kHeadDim;
   Row8 acc = {{0, 0, 0, 0}};
-  for (unsigned pair = ch.x * kNrWarps + (threadIdx.x >> 5); pair < (tokens + 1) / 2; pair += ch.ctas * kNrWarps) {
-    const NormRopeToken k(p, 2 * pair + ((threadIdx.x >> 4) & 1), tokens);
-    if (k.in && !k.fits && k.r == 0 && ch.chunk == 0 && l == 0) atomicOr(&g_device_error, kDevErrCacheFull);
-    float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
-    if (k.live) load_angles(p.table, p.rot, k.t0 + k.r, l, c, s);
+
+  auto fetch_rows = [&](const NormRopeToken& k, int hb, int st) {
     const __nv_bfloat16* x0 = isq ? p.q + k.tok * p.q_stride : p.k + k.tok * p.k_stride;
     const __nv_bfloat16* gq = p.dq + static_cast<size_t>(k.tok) * p.Hq * kHeadDim;
-    const size_t head = static_cast<size_t>(p.Lq) * kHeadDim;
     const size_t go = static_cast<size_t>(k.b) * p.Hkv * head + static_cast<size_t>(k.r) * kHeadDim;
-    for (int hb = h0; hb < h1; hb += kNrBwdRows) {
-      Raw8 rx[kNrBwdRows], rg[kNrBwdRows];
 #pragma unroll
-      for (int u = 0; u < kNrBwdRows; ++u) {
-        const int h = hb + u;
-        rx[u] = rg[u] = {make_uint2(0, 0), make_uint2(0, 0)};
-        if (k.live && h < h1) {
-          if (isq || h < p.Hkv) rx[u] = load_row(x0 + h * kHeadDim, ra, rb);
-          rg[u] = load_row(isq ? gq + h * kHeadDim : h < p.Hkv ? p.dk + go + h * head : p.dv + go + (h - p.Hkv) * head,
-                           ra, rb);
-        }
+    for (int u = 0; u < kNrBwdRows; ++u) {
+      const int h = hb + u * hs;
+      if (h >= h1) break;  // the same for the whole CTA
+      if (isq || h < p.Hkv) {
+        const __nv_bfloat16* x = x0 + h * kHeadDim;
+        copy_async<8>(&S.x[st][u][0][lane], x + ra, k.live);
+        copy_async<8>(&S.x[st][u][1][lane], x + rb, k.live);
       }
-      Turn<kInterleaved> back;
-      back.set(c, s, -1.f);
-#pragma unroll
-      for (int u = 0; u < kNrBwdRows; ++u) {
-        const int h = hb + u;
-        if (h >= h1) break;  // the same for the whole CTA
-        if (!isq && h >= p.Hkv) {
-          if (k.live) store_row(p.v_out + k.tok * p.dv_stride + (h - p.Hkv) * kHeadDim, ra, rb, rg[u]);
-          continue;
-        }
-        const Row8 x = unpack8(rx[u]);
-        Row8 g = unpack8(rg[u]);
-        back.apply(g);
-        Row8 gw;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) gw.v[i] = mul2(g.v[i], w.v[i]);
-        const float ss = half_sum(dot8(x, x)), dot = half_sum(dot8(gw, x));
-        const float rs = rsqrtf(ss * (1.f / kHeadDim) + p.eps);
-        const float k3 = -rs * rs * rs * dot * (1.f / kHeadDim);
-        const uint64_t r2 = f2(rs, rs), n3 = f2(k3, k3);
-        Row8 dx;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          acc.v[i] = fma2(mul2(g.v[i], r2), x.v[i], acc.v[i]);  // rows that are not live are zeros
-          dx.v[i] = fma2(gw.v[i], r2, mul2(x.v[i], n3));
-        }
-        if (k.live)
-          store_row(isq ? p.q_out + k.tok * p.dq_stride + h * kHeadDim : p.k_out + k.tok * p.dk_stride + h * kHeadDim,
-                    ra, rb, pack8(dx));
-      }
+      const __nv_bfloat16* g = isq ? gq + h * kHeadDim : h < p.Hkv ? p.dk + go + h * head : p.dv + go + (h - p.Hkv) * head;
+      copy_async<8>(&S.g[st][u][0][lane], g + ra, k.live);
+      copy_async<8>(&S.g[st][u][1][lane], g + rb, k.live);
     }
+  };
+  auto fetch_token = [&](unsigned pair, int slot, int st) {
+    const NormRopeToken k(p, 2 * pair + ((threadIdx.x >> 4) & 1), tokens);
+    if (k.in && !k.fits && k.r == 0 && ch.chunk == 0 && l == 0) atomicOr(&g_device_error, kDevErrCacheFull);
+    if (8 * l < p.rot) {
+      const float* row = p.table + static_cast<size_t>(k.live ? k.t0 + k.r : 0) * p.rot + 4 * l;
+      copy_async<16>(&S.cs[slot][0][lane], row, k.live);
+      copy_async<16>(&S.cs[slot][1][lane], row + p.rot / 2, k.live);
+    }
+    fetch_rows(k, h0, st);
+    return k;
+  };
+
+  // N rows at once: a row's chain of dependent instructions is longer than its share of the memory's time
+  auto work = [&](auto rows, const NormRopeToken& k, const Turn<kInterleaved>& back, int h, int st, int u) {
+    constexpr int N = decltype(rows)::value;
+    Row8 x[N], g[N], gw[N];
+    float ss[N], dot[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      x[j] = unpack8({S.x[st][u + j][0][lane], S.x[st][u + j][1][lane]});
+      g[j] = unpack8({S.g[st][u + j][0][lane], S.g[st][u + j][1][lane]});
+      back.apply(g[j]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) gw[j].v[i] = mul2(g[j].v[i], w.v[i]);
+      ss[j] = dot8(x[j], x[j]), dot[j] = dot8(gw[j], x[j]);
+    }
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1)
+#pragma unroll
+      for (int j = 0; j < N; ++j) {
+        ss[j] += __shfl_xor_sync(0xffffffffu, ss[j], d, 16);
+        dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], d, 16);
+      }
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const float rs = rsqrtf(ss[j] * (1.f / kHeadDim) + p.eps);
+      const float k3 = -rs * rs * rs * dot[j] * (1.f / kHeadDim);
+      const uint64_t r2 = f2(rs, rs), n3 = f2(k3, k3);
+      Row8 dx;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc.v[i] = fma2(mul2(g[j].v[i], r2), x[j].v[i], acc.v[i]);  // rows that are not live are zeros
+        dx.v[i] = fma2(gw[j].v[i], r2, mul2(x[j].v[i], n3));
+      }
+      const int hj = h + j * hs;
+      if (k.live)
+        store_row(isq ? p.q_out + k.tok * p.dq_stride + hj * kHeadDim : p.k_out + k.tok * p.dk_stride + hj * kHeadDim,
+                  ra, rb, pack8(dx));
+    }
+  };
+
+  unsigned pair = ch.x * kNrWarps + (threadIdx.x >> 5);
+  const unsigned step = ch.ctas * kNrWarps;
+  if (pair < pairs) {
+    int slot = 0, st = 0;
+    NormRopeToken k = fetch_token(pair, 0, 0);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    for (; pair < pairs; pair += step, slot ^= 1) {
+      NormRopeToken next = k;
+      Turn<kInterleaved> back;
+      for (int hb = h0; hb < h1; hb += kNrBwdRows * hs, st ^= 1) {
+        if (hb + kNrBwdRows * hs < h1)
+          fetch_rows(k, hb + kNrBwdRows * hs, st ^ 1);
+        else if (pairs - pair > step)
+          next = fetch_token(pair + step, slot ^ 1, st ^ 1);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        if (hb == h0) {
+          float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
+          if (8 * l < p.rot) {
+            const float4 a = S.cs[slot][0][lane], b = S.cs[slot][1][lane];
+            c[0] = a.x, c[1] = a.y, c[2] = a.z, c[3] = a.w;
+            s[0] = b.x, s[1] = b.y, s[2] = b.z, s[3] = b.w;
+          }
+          back.set(c, s, -1.f);
+        }
+        // the branches are the same for the whole CTA
+        for (int u = 0; u < kNrBwdRows;) {
+          const int h = hb + u * hs;
+          if (h >= h1) break;
+          if (!isq && h >= p.Hkv) {
+            if (k.live)
+              store_row(p.v_out + k.tok * p.dv_stride + (h - p.Hkv) * kHeadDim, ra, rb,
+                        {S.g[st][u][0][lane], S.g[st][u][1][lane]});
+            ++u;
+          } else if (u + 1 < kNrBwdRows && h + hs < hn) {
+            work(std::integral_constant<int, 2>{}, k, back, h, st, u);
+            u += 2;
+          } else {
+            work(std::integral_constant<int, 1>{}, k, back, h, st, u);
+            ++u;
+          }
+        }
+      }
+      k = next;
+    }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
   }
-  __shared__ float red[2 * kNrWarps][kHeadDim];
+  __syncthreads();
+  float(*red)[kHeadDim] = reinterpret_cast<float(*)[kHeadDim]>(nr_smem);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int d = (i < 2 ? ra : rb) + 2 * (i & 1);
@@ -326,7 +435,7 @@ __global__ void __launch_bounds__(kNrThreads, 2) qk_norm_rope_bwd_kernel(const N
     float a = 0.f;
 #pragma unroll
     for (int i = 0; i < 2 * kNrWarps; ++i) a += red[i][threadIdx.x];
-    p.part[(static_cast<size_t>(ch.chunk) * ch.ctas + ch.x) * kHeadDim + threadIdx.x] = a;
+    p.part[static_cast<size_t>(ch.part(p)) * kHeadDim + threadIdx.x] = a;
   }
 }
 
