@@ -291,7 +291,10 @@ int max_active_clusters(void (*kern)(Params...), int C, int threads, size_t smem
   auto it = cache.find(key);
   if (it != cache.end()) return it->second;
   if (set_smem(fn, smem) != INFLLMV2_OK) return 0;
-  if (C > 8 && cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return 0;
+  if (C > 8 && cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return 0;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(C));
   cfg.blockDim = dim3(threads);
@@ -304,7 +307,10 @@ int max_active_clusters(void (*kern)(Params...), int C, int threads, size_t smem
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int active = 0;
-  if (cudaOccupancyMaxActiveClusters(&active, kern, &cfg) != cudaSuccess) active = 0;
+  if (cudaOccupancyMaxActiveClusters(&active, kern, &cfg) != cudaSuccess) {
+    active = 0;
+    (void)cudaGetLastError();  // the caller takes another layout
+  }
   cache.emplace(key, active);
   return active;
 }
