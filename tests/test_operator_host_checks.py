@@ -1,0 +1,50 @@
+"""Host-side checks of the binding for the norm-and-rotation and window-attention calls: they
+come before any CUDA call, so they are tested with tensors of the host."""
+import pytest
+import torch
+
+from trainable_block_sparse_compress_b200 import _lib, build, ops
+
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module", autouse=True)
+def library():
+    build.build()
+
+
+def window_calls(window, n_sink):
+    p = ops.Params(1, 4, 2)
+    q, k = torch.zeros(1, 8, 4, 128, dtype=BF), torch.zeros(1, 2, 8, 128, dtype=BF)
+    lse, lens = torch.zeros(1, 4, 8), torch.ones(1, dtype=torch.int32)
+    yield lambda: ops.window_attn_prefill(p, q, k, k, window, n_sink)
+    yield lambda: ops.window_attn_chunk(p, q, k, k, window, n_sink)
+    yield lambda: ops.window_attn_decode(p, q[:, 0], k, k, lens, window, n_sink)
+    yield lambda: ops.window_attn_backward(p, q, k, k, q, lse, q, window, n_sink)
+
+
+# each of them is a legal number once cut to 32 bits
+@pytest.mark.parametrize("window,n_sink", [(2**32 + 4096, 0), (-(2**32) + 5, 0), (4, 2**32), (4, 2**40 + 1),
+                                           (2**33 + 1, 2**33), (4, -(2**32))])
+def test_numbers_past_32_bits_are_refused_not_cut(window, n_sink):
+    for call in window_calls(window, n_sink):
+        with pytest.raises(_lib.InfLLMv2Error, match="invalid argument"):
+            call()
+
+
+def test_largest_numbers_pass_the_check():
+    for call in window_calls(2**31 - 1, 2**31 - 1):
+        with pytest.raises(ValueError, match="CUDA tensor"):  # the next check
+            call()
+
+
+def test_sizes_past_32_bits_are_refused_not_cut():
+    p = ops.Params(1, 4, 2)
+    with pytest.raises(_lib.InfLLMv2Error, match="invalid argument"):
+        ops.workspace_size(p, _lib.OP_WINDOW_BACKWARD, 2**32 + 100)
+    for field in ("batch", "num_q_heads", "topk", "n_init", "n_local", "score_mode", "pool_mode"):
+        good = dict(batch=1, num_q_heads=4, num_kv_heads=2, topk=16)
+        ops.Params(**good).c()
+        bad = {**good, field: 2**32 + good.get(field, 0)}
+        with pytest.raises(_lib.InfLLMv2Error, match="invalid argument"):
+            ops.Params(**bad).c()

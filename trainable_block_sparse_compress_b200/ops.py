@@ -15,6 +15,11 @@ import torch
 from . import _lib
 
 
+def _is_i32(n) -> bool:
+    """Whether the library's 32-bit argument can hold n (ctypes would cut a larger one)."""
+    return -0x80000000 <= n <= 0x7fffffff
+
+
 @dataclass(frozen=True)
 class Params:
     batch: int
@@ -39,6 +44,9 @@ class Params:
         """The C struct, made once (the fields are frozen; the library only reads it)."""
         c = self.__dict__.get("_c")
         if c is None:
+            for name, kind in _lib.CParams._fields_:
+                if kind is ctypes.c_int32 and not _is_i32(getattr(self, name)):
+                    raise _lib.InfLLMv2Error("infllmv2_check_params", _lib.ERR_INVALID_ARG)
             c = _lib.CParams(self.batch, self.num_q_heads, self.num_kv_heads, self.head_dim, self.block_size,
                              self.kernel_size, self.kernel_stride, self.topk, self.n_init, self.n_local,
                              float(self.softmax_scale), int(self.score_mode), int(self.pool_mode))
@@ -60,6 +68,8 @@ def num_blocks(p: Params, n: int) -> int:
 
 
 def workspace_size(p: Params, op: int, L: int) -> int:
+    if not _is_i32(L):
+        raise _lib.InfLLMv2Error("infllmv2_workspace_size", _lib.ERR_INVALID_ARG)
     v = int(_lib.load().infllmv2_workspace_size(ctypes.byref(p.c()), op, L))
     if v == ctypes.c_size_t(-1).value:
         raise _lib.InfLLMv2Error("infllmv2_workspace_size", _lib.ERR_INVALID_ARG)
@@ -487,6 +497,12 @@ def qk_norm_rope_backward(p: Params, q: torch.Tensor, k: torch.Tensor, d_q: torc
     return dq, dk, dv, d_qw, d_kw
 
 
+def _need_window(fn: str, window: int, n_sink: int) -> None:
+    """The library's own check, made before the numbers become 32-bit arguments."""
+    if not (1 <= window <= 0x7fffffff and 0 <= n_sink <= 0x7fffffff):
+        raise _lib.InfLLMv2Error(fn, _lib.ERR_INVALID_ARG)
+
+
 def window_attn_chunk(p: Params, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int, n_sink: int = 0,
                       q_lens: Optional[torch.Tensor] = None, kv_lens: Optional[torch.Tensor] = None,
                       out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
@@ -496,6 +512,7 @@ def window_attn_chunk(p: Params, q: torch.Tensor, k: torch.Tensor, v: torch.Tens
     are the last q_lens[b] of kv_lens[b] cached tokens) over caches k, v bf16 [B, Hkv, Lmax, d]:
     the query at position t sees the keys u <= t with u > t - window or u < n_sink.  O bf16
     [B, Lq, Hq, d], lse fp32 [B, Hq, Lq] (padding rows not written)."""
+    _need_window("infllmv2_window_attn", window, n_sink)
     B, Lq, Hq, d = q.shape
     Lmax = k.shape[2]
     _need(q, "q", torch.bfloat16, (p.batch, Lq, p.num_q_heads, p.head_dim))
@@ -542,6 +559,7 @@ def window_attn_decode(p: Params, q: torch.Tensor, k_cache: torch.Tensor, v_cach
     """Sliding-window attention of one token per sequence at position lens[b]-1: q bf16
     [B, Hq, d], caches [B, Hkv, Lmax, d] -> O [B, Hq, d], lse fp32 [B, Hq] (0 and -inf for an
     empty sequence)."""
+    _need_window("infllmv2_window_attn_decode", window, n_sink)
     Lmax = k_cache.shape[2]
     _need(q, "q", torch.bfloat16, (p.batch, p.num_q_heads, p.head_dim))
     kv_shape = (p.batch, p.num_kv_heads, Lmax, p.head_dim)
@@ -573,6 +591,7 @@ def window_attn_backward(p: Params, q: torch.Tensor, k: torch.Tensor, v: torch.T
     """Gradients of the window attention over fresh sequences of lens[b] tokens (None: L): q, o,
     d_o bf16 [B, L, Hq, d], k, v bf16 [B, Hkv, L, d], lse fp32 [B, Hq, L] from the forward ->
     dq [B, L, Hq, d], dk, dv [B, Hkv, L, d] (bf16; rows of padding are not written)."""
+    _need_window("infllmv2_window_attn_backward", window, n_sink)
     B, L, Hq, d = q.shape
     for t, name in ((q, "q"), (o, "o"), (d_o, "d_o")):
         _need(t, name, torch.bfloat16, (p.batch, L, p.num_q_heads, p.head_dim))
