@@ -48,3 +48,13 @@ def test_sizes_past_32_bits_are_refused_not_cut():
         bad = {**good, field: 2**32 + good.get(field, 0)}
         with pytest.raises(_lib.InfLLMv2Error, match="invalid argument"):
             ops.Params(**bad).c()
+
+
+@pytest.mark.parametrize("ws", [torch.empty(1 << 20, dtype=torch.uint8), torch.empty(1, dtype=torch.uint8).expand(1 << 20)])
+@pytest.mark.parametrize("op", [_lib.OP_SELECT_DECODE, _lib.OP_ATTN_DECODE, _lib.OP_ATTN_BACKWARD,
+                                _lib.OP_QK_NORM_ROPE_BACKWARD, _lib.OP_WINDOW_ATTN, _lib.OP_WINDOW_DECODE,
+                                _lib.OP_WINDOW_BACKWARD])
+def test_a_workspace_of_the_host_is_refused(ws, op):
+    # the kernels would write to its address
+    with pytest.raises(ValueError, match="ws must be a CUDA tensor"):
+        ops._workspace(ops.Params(1, 4, 2), op, 100, ws, torch.empty(1))

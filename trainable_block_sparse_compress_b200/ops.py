@@ -124,6 +124,9 @@ def _need(t: torch.Tensor, name: str, dtype, shape=None):
 
 
 def _workspace(p: Params, op: int, L: int, ws: Optional[torch.Tensor], like: torch.Tensor) -> Optional[torch.Tensor]:
+    """`ws` (any dtype and shape), or a fresh workspace where it is None or too small."""
+    if ws is not None:
+        _need(ws, "ws", ws.dtype, ws.shape)
     n = _workspace_bytes(p, op, L)
     if n == 0:
         return ws
