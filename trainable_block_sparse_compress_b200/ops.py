@@ -465,8 +465,8 @@ def qk_norm_rope_backward(p: Params, q: torch.Tensor, k: torch.Tensor, d_q: torc
     """Gradients of qk_norm_rope's inputs: q, k as given to it, d_q bf16 [B, Lq, Hq, d], d_k, d_v
     [B, Hkv, Lq, d] (the layouts sparse_attn_backward and window_attn_backward return).  Returns
     (dq, dk, dv, d_qw, d_kw): token rows [B, Lq, H, d], views of one packed tensor
-    [B, Lq, Hq + 2 Hkv, d] (`out`, allocated when None; rows of padding are not written), and the
-    weights' gradients, fp32 [d] (None for a weight that is None)."""
+    [B, Lq, Hq + 2 Hkv, d] (`out`: rows of padding are not written; allocated when None: they are
+    zero), and the weights' gradients, fp32 [d] (None for a weight that is None)."""
     B, Lq = q.shape[:2]
     Hq, Hkv, d = p.num_q_heads, p.num_kv_heads, p.head_dim
     qs = _need_tokens(q, "q", p.batch, Lq, Hq, d)
@@ -483,7 +483,9 @@ def qk_norm_rope_backward(p: Params, q: torch.Tensor, k: torch.Tensor, d_q: torc
     if q_lens is not None:
         _need(q_lens, "q_lens", torch.int32, (B,))
     if out is None:
-        out = q.new_empty((B, Lq, Hq + 2 * Hkv, d))
+        # the rows go into the projection's weight gradient: none may hold what was in memory
+        make = q.new_empty if q_lens is None else q.new_zeros
+        out = make((B, Lq, Hq + 2 * Hkv, d))
     else:
         _need(out, "out", torch.bfloat16, (B, Lq, Hq + 2 * Hkv, d))
     dq, dk, dv = out.split((Hq, Hkv, Hkv), 2)
@@ -593,7 +595,8 @@ def window_attn_backward(p: Params, q: torch.Tensor, k: torch.Tensor, v: torch.T
                          dv: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """Gradients of the window attention over fresh sequences of lens[b] tokens (None: L): q, o,
     d_o bf16 [B, L, Hq, d], k, v bf16 [B, Hkv, L, d], lse fp32 [B, Hq, L] from the forward ->
-    dq [B, L, Hq, d], dk, dv [B, Hkv, L, d] (bf16; rows of padding are not written)."""
+    dq [B, L, Hq, d], dk, dv [B, Hkv, L, d] (bf16; rows of padding are not written in tensors that
+    are given, and zero in those allocated here)."""
     _need_window("infllmv2_window_attn_backward", window, n_sink)
     B, L, Hq, d = q.shape
     for t, name in ((q, "q"), (o, "o"), (d_o, "d_o")):
@@ -606,9 +609,10 @@ def window_attn_backward(p: Params, q: torch.Tensor, k: torch.Tensor, v: torch.T
     for t, ref, name in ((dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv")):
         if t is not None:
             _need(t, name, torch.bfloat16, ref.shape)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    make = torch.empty_like if lens is None else torch.zeros_like
+    dq = make(q) if dq is None else dq
+    dk = make(k) if dk is None else dk
+    dv = make(v) if dv is None else dv
     ws = _workspace(p, _lib.OP_WINDOW_BACKWARD, L, ws, q)
     nbytes = 0 if ws is None else ws.numel() * ws.element_size()
     st = _lib.load().infllmv2_window_attn_backward(ctypes.byref(p.c()), _ptr(q), _ptr(k), _ptr(v), _ptr(o), _ptr(lse),
