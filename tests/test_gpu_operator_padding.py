@@ -58,3 +58,28 @@ def test_gradients_of_padding_are_zero_in_tensors_made_by_the_calls():
     # what a training step does next: the projection's weight gradient over all rows
     packed = torch.cat(r[:3], 2).view(B * L, -1)
     assert torch.isfinite(packed.T.float() @ torch.ones(B * L, 16, device="cuda")).all()
+
+
+def test_forward_rows_of_padding_are_zero_in_tensors_made_by_the_calls():
+    g = torch.Generator(device="cuda").manual_seed(2)
+    p = ops.Params(B, HQ, HKV)
+    lens = torch.tensor(LENS, dtype=torch.int32, device="cuda")
+    table = ops.rope_table(p, 1e4 ** (-torch.arange(64, device="cuda") / 64), L)
+    x = randn(g, B, L, HQ + 2 * HKV, 128)
+    poison()
+    q, k, v = ops.qk_norm_rope(p, x[:, :, :HQ], x[:, :, HQ:HQ + HKV], x[:, :, HQ + HKV:], table, q_lens=lens)
+    for y in (q, k.transpose(1, 2), v.transpose(1, 2)):
+        assert (padding(y) == 0).all()
+    poison()
+    o, _ = ops.window_attn_chunk(p, q, k, v, 100, 4, q_lens=lens, kv_lens=lens)
+    assert (padding(o) == 0).all()
+    # the same rows as in tensors of the caller, whose padding is left alone
+    mine = [torch.full_like(y, 7.0) for y in (q, k, v, o)]
+    ops.qk_norm_rope(p, x[:, :, :HQ], x[:, :, HQ:HQ + HKV], x[:, :, HQ + HKV:], table, q_lens=lens, q_out=mine[0],
+                     k_out=mine[1], v_out=mine[2])
+    ops.window_attn_chunk(p, mine[0], mine[1], mine[2], 100, 4, q_lens=lens, kv_lens=lens, out=mine[3])
+    for got, m in zip((q, k.transpose(1, 2), v.transpose(1, 2), o),
+                      (mine[0], mine[1].transpose(1, 2), mine[2].transpose(1, 2), mine[3])):
+        assert (padding(m) == 7.0).all()
+        for b in range(B):
+            assert torch.equal(got[b, :LENS[b]], m[b, :LENS[b]])

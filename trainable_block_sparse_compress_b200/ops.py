@@ -410,7 +410,8 @@ def qk_norm_rope(p: Params, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, t
     rows at or past q_lens[b] are padding.  Returns q [B, Lq, Hq, d] and k, v: with k_cache and
     v_cache [B, Hkv, Lmax, d], the caches with the rows written at their positions; otherwise
     [B, Hkv, Lq, d] (with Lq = 1, q[:, 0], k[:, :, 0] and v[:, :, 0] are what decode_step
-    takes).  lens_out int32 [B], when given, receives starts[b] + the sequence's rows."""
+    takes).  Rows of padding are zero in outputs made here and not written in those given.
+    lens_out int32 [B], when given, receives starts[b] + the sequence's rows."""
     B, Lq = q.shape[:2]
     qs = _need_tokens(q, "q", p.batch, Lq, p.num_q_heads, p.head_dim)
     ks = _need_tokens(k, "k", p.batch, Lq, p.num_kv_heads, p.head_dim)
@@ -426,9 +427,10 @@ def qk_norm_rope(p: Params, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, t
         _need(lens_out, "lens_out", torch.int32, (B,))
     if (k_cache is None) != (v_cache is None):
         raise ValueError("k_cache and v_cache go together")
-    # outputs made here need no checks
+    # outputs made here need no checks; their rows of padding reach calls that take no lengths
+    make = q.new_empty if q_lens is None else q.new_zeros
     if q_out is None:
-        q_out = q.new_empty((B, Lq, p.num_q_heads, p.head_dim))
+        q_out = make((B, Lq, p.num_q_heads, p.head_dim))
     else:
         _need(q_out, "q_out", torch.bfloat16, (B, Lq, p.num_q_heads, p.head_dim))
     if k_cache is not None:
@@ -444,11 +446,11 @@ def qk_norm_rope(p: Params, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, t
         if k_out is not None:
             _need(k_out, "k_out", torch.bfloat16, kv_shape)
         else:
-            k_out = q.new_empty(kv_shape)
+            k_out = make(kv_shape)
         if v_out is not None:
             _need(v_out, "v_out", torch.bfloat16, kv_shape)
         else:
-            v_out = torch.empty_like(k_out)
+            v_out = make(kv_shape)
     st = _lib.load().infllmv2_qk_norm_rope(ctypes.byref(p.c()), _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, Lq,
                                            _ptr(q_weight), _ptr(k_weight), wf, eps, _ptr(table), n, rot,
                                            int(interleaved), _ptr(starts), _ptr(q_lens), _ptr(q_out), _ptr(k_out),
@@ -516,7 +518,8 @@ def window_attn_chunk(p: Params, q: torch.Tensor, k: torch.Tensor, v: torch.Tens
     """Sliding-window attention of a chunk of queries (as sparse_attn_chunk: rows 0..q_lens[b]-1
     are the last q_lens[b] of kv_lens[b] cached tokens) over caches k, v bf16 [B, Hkv, Lmax, d]:
     the query at position t sees the keys u <= t with u > t - window or u < n_sink.  O bf16
-    [B, Lq, Hq, d], lse fp32 [B, Hq, Lq] (padding rows not written)."""
+    [B, Lq, Hq, d], lse fp32 [B, Hq, Lq] (padding rows not written; with q_lens those of an O made
+    here are zero, as the output projection's weight gradient runs over them)."""
     _need_window("infllmv2_window_attn", window, n_sink)
     B, Lq, Hq, d = q.shape
     Lmax = k.shape[2]
@@ -529,7 +532,7 @@ def window_attn_chunk(p: Params, q: torch.Tensor, k: torch.Tensor, v: torch.Tens
     if kv_lens is not None:
         _need(kv_lens, "kv_lens", torch.int32, (p.batch,))
     if out is None:
-        out = torch.empty_like(q)
+        out = torch.empty_like(q) if q_lens is None else torch.zeros_like(q)
     else:
         _need(out, "o", torch.bfloat16, q.shape)
     if lse is not None:
