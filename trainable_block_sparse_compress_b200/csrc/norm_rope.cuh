@@ -361,13 +361,15 @@ __global__ void __launch_bounds__(kNrThreads, kNrBwdCtas) qk_norm_rope_bwd_kerne
 #pragma unroll
     for (int j = 0; j < N; ++j) {
       const float rs = rsqrtf(ss[j] * (1.f / kHeadDim) + p.eps);
-      const float k3 = -rs * rs * rs * dot[j] * (1.f / kHeadDim);
-      const uint64_t r2 = f2(rs, rs), n3 = f2(k3, k3);
+      // dx = r (g w - (x r) r mean(g w x)): no power of r, which for a tiny row and eps leaves fp32's range
+      const float t = -rs * dot[j] * (1.f / kHeadDim);
+      const uint64_t r2 = f2(rs, rs), t2 = f2(t, t);
       Row8 dx;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        acc.v[i] = fma2(mul2(g[j].v[i], r2), x[j].v[i], acc.v[i]);  // rows that are not live are zeros
-        dx.v[i] = fma2(gw[j].v[i], r2, mul2(x[j].v[i], n3));
+        const uint64_t xr = mul2(x[j].v[i], r2);
+        acc.v[i] = fma2(g[j].v[i], xr, acc.v[i]);  // rows that are not live are zeros
+        dx.v[i] = mul2(fma2(xr, t2, gw[j].v[i]), r2);
       }
       const int hj = h + j * hs;
       if (k.live)
