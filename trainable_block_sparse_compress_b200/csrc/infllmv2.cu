@@ -155,6 +155,12 @@ constexpr size_t kMaxSmem = 227 * 1024;
 
 int launch_status() { return cudaGetLastError() == cudaSuccess ? INFLLMV2_OK : INFLLMV2_ERR_CUDA; }
 
+// The status of a runtime call that failed: reported here, not by the next call's launch_status().
+int cuda_failed() {
+  (void)cudaGetLastError();
+  return INFLLMV2_ERR_CUDA;
+}
+
 constexpr int kMaxCachedDevices = 64;
 
 // Multiprocessors of the current device (looked up once per device).
@@ -172,21 +178,61 @@ int set_smem(const void* fn, size_t bytes) {
   return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) ==
                  cudaSuccess
              ? INFLLMV2_OK
-             : INFLLMV2_ERR_CUDA;
+             : cuda_failed();
+}
+
+// Clusters of C CTAs of `kern` that the device holds at once (cached per kernel, size, threads,
+// shared memory and device), or -1 when a runtime call fails.
+template <typename... Params>
+int max_active_clusters(void (*kern)(Params...), int C, int threads, size_t smem) {
+  static std::mutex mu;
+  static std::map<std::tuple<const void*, int, int, size_t, int>, int> cache;
+  const void* fn = reinterpret_cast<const void*>(kern);
+  int dev = 0, active = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return cuda_failed(), -1;
+  std::lock_guard<std::mutex> lock(mu);
+  const auto key = std::make_tuple(fn, C, threads, smem, dev);
+  auto it = cache.find(key);
+  if (it != cache.end()) return it->second;
+  if (set_smem(fn, smem) != INFLLMV2_OK) return -1;
+  if (C > 8 && cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+    return cuda_failed(), -1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(C));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(C);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaOccupancyMaxActiveClusters(&active, kern, &cfg);
+  if (e != cudaSuccess) {
+    (void)cuda_failed();
+    if (e != cudaErrorInvalidClusterSize) return -1;
+    active = 0;  // a size that the device cannot hold
+  }
+  cache.emplace(key, active);
+  return active;
 }
 
 // Launches `kern` on a 1-D grid in clusters of C CTAs.  Sizes above 8 need the
 // non-portable opt-in.  With `pdl` the kernel may start while the previous kernel on the
-// stream finishes (it must call grid_dependency_wait() before reading any input).  A cluster shape that the device cannot co-schedule is reported
-// as unsupported before any launch (checked once per kernel, size and device).
+// stream finishes (it must call grid_dependency_wait() before reading any input).  A cluster
+// shape that the device cannot co-schedule is reported as unsupported before any launch.
 template <typename... Params, typename... Args>
 int launch_cluster(void (*kern)(Params...), unsigned grid, int C, int threads, size_t smem, cudaStream_t s,
                    bool pdl, Args&&... args) {
+  const int fits = max_active_clusters(kern, C, threads, smem);
+  if (fits < 0) return INFLLMV2_ERR_CUDA;
+  if (fits < 1) return INFLLMV2_ERR_UNSUPPORTED;
   const void* fn = reinterpret_cast<const void*>(kern);
   int st = set_smem(fn, smem);
   if (st != INFLLMV2_OK) return st;
   if (C > 8 && cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-    return INFLLMV2_ERR_CUDA;
+    return cuda_failed();
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
@@ -201,23 +247,7 @@ int launch_cluster(void (*kern)(Params...), unsigned grid, int C, int threads, s
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 2 : 1;
-  {
-    static std::mutex mu;
-    static std::map<std::tuple<const void*, int, int>, int> fits;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return INFLLMV2_ERR_CUDA;
-    std::lock_guard<std::mutex> lock(mu);
-    const auto key = std::make_tuple(fn, C, dev);
-    auto it = fits.find(key);
-    if (it == fits.end()) {
-      int active = 0;
-      if (cudaOccupancyMaxActiveClusters(&active, kern, &cfg) != cudaSuccess) return INFLLMV2_ERR_CUDA;
-      it = fits.emplace(key, active).first;
-    }
-    if (it->second < 1) return INFLLMV2_ERR_UNSUPPORTED;
-  }
-  if (cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...) != cudaSuccess) return INFLLMV2_ERR_CUDA;
-  return launch_status();
+  return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...) == cudaSuccess ? INFLLMV2_OK : cuda_failed();
 }
 
 // Launches `kern` so that it may start while the previous kernel on the stream finishes (it
@@ -234,9 +264,7 @@ int launch_pdl(void (*kern)(Params...), dim3 grid, int threads, size_t smem, cud
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...) == cudaSuccess) return INFLLMV2_OK;
-  (void)cudaGetLastError();  // reported here, not by the next call
-  return INFLLMV2_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...) == cudaSuccess ? INFLLMV2_OK : cuda_failed();
 }
 
 // Decode work layout.  Each (sequence, kv-head) item's selected blocks are split over
@@ -275,44 +303,6 @@ int select_cluster(const infllmv2_params* p, int64_t nk) {
   int c = 1;
   while (c < kSdMaxCluster && (static_cast<int64_t>(c) * kSdMaxChunk < nk || items * c * 2 <= target)) c *= 2;
   return c;
-}
-
-// Clusters of C CTAs of `kern` that the device holds at once (cached per kernel, size,
-// shared memory and device).
-template <typename... Params>
-int max_active_clusters(void (*kern)(Params...), int C, int threads, size_t smem) {
-  static std::mutex mu;
-  static std::map<std::tuple<const void*, int, size_t, int>, int> cache;
-  const void* fn = reinterpret_cast<const void*>(kern);
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  std::lock_guard<std::mutex> lock(mu);
-  const auto key = std::make_tuple(fn, C, smem, dev);
-  auto it = cache.find(key);
-  if (it != cache.end()) return it->second;
-  if (set_smem(fn, smem) != INFLLMV2_OK) return 0;
-  if (C > 8 && cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
-    (void)cudaGetLastError();
-    return 0;
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(C));
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(C);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  int active = 0;
-  if (cudaOccupancyMaxActiveClusters(&active, kern, &cfg) != cudaSuccess) {
-    active = 0;
-    (void)cudaGetLastError();  // the caller takes another layout
-  }
-  cache.emplace(key, active);
-  return active;
 }
 
 // Decode-step cluster size: enough CTAs for the longest sequence's kernels (at most
