@@ -1,5 +1,8 @@
 """Host-side checks of the binding for the norm-and-rotation and window-attention calls: they
 come before any CUDA call, so they are tested with tensors of the host."""
+import os
+import re
+
 import pytest
 import torch
 
@@ -58,3 +61,27 @@ def test_a_workspace_of_the_host_is_refused(ws, op):
     # the kernels would write to its address
     with pytest.raises(ValueError, match="ws must be a CUDA tensor"):
         ops._workspace(ops.Params(1, 4, 2), op, 100, ws, torch.empty(1))
+
+
+# The copying thread of each window kernel: a copy that lands after its CTA has ended writes into
+# the next CTA's shared memory.  No timeout is provoked on the GPU; the sources are read instead.
+COPIERS = [("window_tc.cuh", "window_tc_kernel"), ("window_bwd_tc.cuh", "window_dkdv"), ("window_bwd_tc.cuh", "window_dq"),
+           ("window_decode.cuh", "window_decode_kernel")]
+
+
+@pytest.mark.parametrize("file,fn", COPIERS)
+def test_copying_threads_wait_for_every_copy_before_they_return(file, fn):
+    src = open(os.path.join(build.CSRC, file)).read()
+    body = src[re.search(rf"\n\s*(__device__ __forceinline__ void )?{fn}\(", src).start():]
+    body = body[:body.index("\n}\n")]
+    armed = set(re.findall(r"mbar_arrive_expect_tx\(&S\.(\w+)", body))
+    for either in re.findall(r"uint64_t\* bar = any \? &S\.(.*?) : &S\.(\w+)", body):
+        armed |= {re.sub(r"\[0\]$", "", either[0]), either[1]}
+    assert armed, "the kernel arms no barrier"
+    last = max(m.end() for m in re.finditer(r"tma_load_\dd\(", body))
+    tail = body[last:]
+    tail = tail[:re.search(r"\n    return;|__syncwarp\(\);\n  \}", tail).end()]
+    assert "if (S.abort && lane == 0)" not in tail, "waits for its copies only when a wait has been given up already"
+    waited = {re.sub(r"\[0\]$|\[x\]$", "", x) for x in re.findall(r"mbar_wait_drain\(&S\.([\w\[\]]+)", tail)}
+    waited |= set(re.findall(r"drain_ring\(S\.(\w+)", tail))
+    assert waited == armed

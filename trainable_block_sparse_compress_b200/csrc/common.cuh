@@ -144,6 +144,14 @@ __device__ __forceinline__ bool mbar_wait_drain(uint64_t* bar, uint32_t parity) 
   }
 }
 
+// The last wait of a copying thread: its `issued` copies went to a ring of kSlots barriers in turn,
+// and none may land after the CTA has given its shared memory up, whichever warp gave up a wait.
+template <int kSlots>
+__device__ __forceinline__ void drain_ring(uint64_t (&full)[kSlots], int issued) {
+  for (int s = 0; s < kSlots; ++s)
+    if (issued > s) mbar_wait_drain(&full[s], static_cast<uint32_t>((issued - 1 - s) / kSlots) & 1u);
+}
+
 // ---------------------------------------------------------------------- TMA
 
 // 2-D tiled bulk tensor load global -> shared, completion counted in bytes on `bar`.

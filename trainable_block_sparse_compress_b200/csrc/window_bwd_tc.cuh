@@ -245,8 +245,9 @@ __device__ __forceinline__ void window_dkdv(const CUtensorMap& tm_q, const CUten
     }
     const size_t stat0 = (static_cast<size_t>(bg) * p.Lp + ta) << p.g_log2;
     int slot = 0, issued = 0;
-    uint32_t stats = 0;
-    bool tail_used = false, stop = false;
+    int stats = 0;
+    uint32_t tails = 0;
+    bool stop = false;
     for (int i = 0; i < n && !stop; ++i) {
       const int o = tile_at(i), t0 = ta + o * tt;
       const bool any = w.q_lens != nullptr && t0 + tt > len;  // rows past the end may hold anything
@@ -280,7 +281,7 @@ __device__ __forceinline__ void window_dkdv(const CUtensorMap& tm_q, const CUten
         if (kd == 0) ++stats;
         ++issued;
         if (any) {
-          tail_used = true;
+          tails |= 1u << kd;
           if (mbar_wait_short(&S.tail[kd], 0, &S.abort)) zero_tile_rows(dst, (len - t0) << p.g_log2, lane);
           fence_proxy_async_smem();
           __syncwarp();
@@ -290,13 +291,12 @@ __device__ __forceinline__ void window_dkdv(const CUtensorMap& tm_q, const CUten
         if (++slot == kWbSlots) slot = 0;
       }
     }
-    if (S.abort && lane == 0) {  // let every copy this thread issued land before the CTA ends
+    if (lane == 0) {  // every copy this thread issued lands before the CTA ends
       mbar_wait_drain(&S.res_full, 0);
-      for (int s = 0; s < kWbSlots; ++s)
-        if (issued > s) mbar_wait_drain(&S.full[s], static_cast<uint32_t>((issued - 1 - s) / kWbSlots) & 1u);
-      for (uint32_t s = 0; s < 2; ++s)
-        if (stats > s) mbar_wait_drain(&S.st_full[s], ((stats - 1u - s) / 2) & 1u);
-      if (tail_used) mbar_wait_drain(&S.tail[0], 0);
+      for (int kd = 0; kd < 2; ++kd)
+        if ((tails >> kd) & 1u) mbar_wait_drain(&S.tail[kd], 0);
+      drain_ring(S.full, issued);
+      drain_ring(S.st_full, stats);
     }
     return;
   }
@@ -602,11 +602,10 @@ __device__ __forceinline__ void window_dq(const CUtensorMap& tm_q, const CUtenso
         __syncwarp();
         if (++slot == kWbSlots) slot = 0;
       }
-    if (S.abort && lane == 0) {
+    if (lane == 0) {  // every copy this thread issued lands before the CTA ends
       mbar_wait_drain(&S.res_full, 0);
-      for (int s = 0; s < kWbSlots; ++s)
-        if (issued > s) mbar_wait_drain(&S.full[s], static_cast<uint32_t>((issued - 1 - s) / kWbSlots) & 1u);
       if (tail_used) mbar_wait_drain(&S.tail[0], 0);
+      drain_ring(S.full, issued);
     }
     return;
   }

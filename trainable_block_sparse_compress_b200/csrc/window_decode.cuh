@@ -93,14 +93,11 @@ __global__ void __launch_bounds__(kWdThreads, 2)
 
   if (warp == kWdWarps) {
     if (lane == 0) {
-      for (int i = 0; i < n; ++i) {
+      int i = 0;
+      for (; i < n; ++i) {
         const int st = i % kWdStages, seg = s0 + i;
         if (i >= kWdStages) mbar_wait_short(&S.empty[st], static_cast<uint32_t>(i / kWdStages - 1) & 1u, &S.abort);
-        if (S.abort) {  // let every copy this thread issued land before the CTA ends
-          for (int s = 0; s < kWdStages; ++s)
-            if (i > s) mbar_wait_drain(&S.full[s], static_cast<uint32_t>((i - 1 - s) / kWdStages) & 1u);
-          break;
-        }
+        if (S.abort) break;
         unsigned char* dst = ring + st * kWdStageBytes;
         const bool sink = runs.is_sink(seg);
         const int key = runs.first_key(seg);
@@ -110,6 +107,7 @@ __global__ void __launch_bounds__(kWdThreads, 2)
           tma_load_3d(dst + (2 + h) * kWdHalf, sink ? &tm_vs : &tm_v, &S.full[st], 64 * h, key, bg);
         }
       }
+      drain_ring(S.full, i);  // every copy lands before the ring is used for the joins and the CTA ends
     }
     __syncwarp();
   }

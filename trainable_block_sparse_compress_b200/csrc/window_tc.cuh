@@ -294,12 +294,11 @@ __global__ void __launch_bounds__(kWfThreads, 1)
         __syncwarp();
         if (++slot == kWfSlots) slot = 0;
       }
-    if (S.abort && lane == 0) {  // let every copy this thread issued land before the CTA ends
+    if (lane == 0) {  // every copy this thread issued lands before the CTA ends
       for (int x = 0; x < (kPaired ? 1 : 2); ++x)
         if (je[x] > jb[x]) mbar_wait_drain(&S.q_full[x], 0);
-      for (int s = 0; s < kWfSlots; ++s)
-        if (issued > s) mbar_wait_drain(&S.full[s], static_cast<uint32_t>((issued - 1 - s) / kWfSlots) & 1u);
       if (tail_used) mbar_wait_drain(&S.tail, 0);
+      drain_ring(S.full, issued);
     }
     return;
   }
