@@ -442,7 +442,8 @@ INFLLMV2_API int infllmv2_window_attn_decode(const infllmv2_params* p, const voi
  *              from infllmv2_window_attn with q_lens = kv_lens = lens)
  *   lens       int32 [B] device or NULL: sequence b holds lens[b] tokens (clamped to [0, L]);
  *              rows at or past lens[b] are padding: not read, and their gradients not written
- *   dq         bf16 [B, L, Hq, d];  dk, dv bf16 [B, Hkv, L, d] (outputs)
+ *   dq         bf16 [B, L, Hq, d];  dk, dv bf16 [B, Hkv, L, d] (outputs; INVALID_ARG when one
+ *              overlaps q, k, v, d_o or another output: the kernels still read those)
  *   ws         at least infllmv2_workspace_size(p, INFLLMV2_OP_WINDOW_BACKWARD, L) bytes
  *              (contents on entry do not matter; calls that overlap on the GPU need one each)
  * Deterministic: no atomics, every sum in a fixed order.  UNSUPPORTED past 65535 (sequence,

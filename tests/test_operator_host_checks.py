@@ -1,5 +1,6 @@
 """Host-side checks of the binding for the norm-and-rotation and window-attention calls: they
 come before any CUDA call, so they are tested with tensors of the host."""
+import ctypes
 import os
 import re
 
@@ -85,3 +86,18 @@ def test_copying_threads_wait_for_every_copy_before_they_return(file, fn):
     waited = {re.sub(r"\[0\]$|\[x\]$", "", x) for x in re.findall(r"mbar_wait_drain\(&S\.([\w\[\]]+)", tail)}
     waited |= set(re.findall(r"drain_ring\(S\.(\w+)", tail))
     assert waited == armed
+
+
+# dq, dk and dv are written while other CTAs still read the inputs: in place would be a race
+@pytest.mark.parametrize("out,other", [(o, i) for o in ("dq", "dk", "dv") for i in ("q", "k", "v", "d_o")] + [
+    ("dk", "dq"), ("dv", "dq"), ("dv", "dk")])
+@pytest.mark.parametrize("shift", [0, -256, 256])
+def test_window_backward_in_place_is_refused(out, other, shift):
+    p = ops.Params(2, 8, 2)
+    # addresses far apart, never read: nothing is launched
+    at = {n: (i + 1) << 24 for i, n in enumerate(("q", "k", "v", "o", "lse", "d_o", "dq", "dk", "dv", "ws"))}
+    at[out] = at[other] + shift
+    st = _lib.load().infllmv2_window_attn_backward(
+        ctypes.byref(p.c()), at["q"], at["k"], at["v"], at["o"], at["lse"], at["d_o"], None, 128, 16, 4, at["dq"],
+        at["dk"], at["dv"], at["ws"], 1 << 40, None)
+    assert st == _lib.ERR_INVALID_ARG

@@ -9,6 +9,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 #include <map>
 #include <mutex>
 #include <tuple>
@@ -484,6 +485,11 @@ size_t ws_size(const infllmv2_params* p, int op, int32_t L) {
 }
 
 int check_chunk(int32_t Lq, const int32_t* q_lens, const int32_t* kv_lens, int32_t Lmax);
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + nb && y < x + na;
+}
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
@@ -1379,6 +1385,14 @@ int infllmv2_window_attn_backward(const infllmv2_params* p, const void* q, const
     return INFLLMV2_ERR_INVALID_ARG;
   const size_t need = ws_size(p, INFLLMV2_OP_WINDOW_BACKWARD, L);
   if (need > 0 && (ws == nullptr || ws_bytes < need || !aligned16(ws))) return INFLLMV2_ERR_WORKSPACE;
+  // dq and dk / dv are written while other CTAs still read these
+  const size_t row = static_cast<size_t>(p->batch) * L * kHeadDim * sizeof(__nv_bfloat16);
+  const size_t qn = row * p->num_q_heads, kn = row * p->num_kv_heads;
+  for (const void* x : {q, d_o})
+    if (overlap(dq, qn, x, qn) || overlap(dk, kn, x, qn) || overlap(dv, kn, x, qn)) return INFLLMV2_ERR_INVALID_ARG;
+  for (const void* x : {k, v})
+    if (overlap(dq, qn, x, kn) || overlap(dk, kn, x, kn) || overlap(dv, kn, x, kn)) return INFLLMV2_ERR_INVALID_ARG;
+  if (overlap(dq, qn, dk, kn) || overlap(dq, qn, dv, kn) || overlap(dk, kn, dv, kn)) return INFLLMV2_ERR_INVALID_ARG;
   a.o_in = static_cast<const __nv_bfloat16*>(o);
   a.lse = const_cast<float*>(lse);
   a.d_o = static_cast<const __nv_bfloat16*>(d_o);

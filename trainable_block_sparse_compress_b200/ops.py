@@ -599,7 +599,8 @@ def window_attn_backward(p: Params, q: torch.Tensor, k: torch.Tensor, v: torch.T
     """Gradients of the window attention over fresh sequences of lens[b] tokens (None: L): q, o,
     d_o bf16 [B, L, Hq, d], k, v bf16 [B, Hkv, L, d], lse fp32 [B, Hq, L] from the forward ->
     dq [B, L, Hq, d], dk, dv [B, Hkv, L, d] (bf16; rows of padding are not written in tensors that
-    are given, and zero in those allocated here)."""
+    are given, and zero in those allocated here).  dq, dk and dv, when given, must not overlap
+    q, k, v, d_o or one another."""
     _need_window("infllmv2_window_attn_backward", window, n_sink)
     B, L, Hq, d = q.shape
     for t, name in ((q, "q"), (o, "o"), (d_o, "d_o")):
