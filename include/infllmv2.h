@@ -365,7 +365,7 @@ INFLLMV2_API int infllmv2_rope_table(const infllmv2_params* p, const float* inv_
  *   q_out      bf16 [B, Lq, Hq, d]
  *   k_out, v_out  bf16 [B, Hkv, Lout, d]; at_position = 0: row r of sequence b goes to row r
  *              (Lout >= Lq); at_position = 1: to row starts[b] + r (caches, Lout = Lmax)
- *   lens_out   int32 [B] device or NULL: starts[b] + the sequence's rows; not starts itself
+ *   lens_out   int32 [B] device or NULL: starts[b] + the sequence's rows; not starts or q_lens
  * A sequence whose rows leave the table (starts[b] < 0, or starts[b] + rows > table_rows) or, at
  * position, the caches (> Lout) is left untouched (lens_out[b] = starts[b]) and sets
  * INFLLMV2_DEVERR_CACHE_FULL in the device error word.  Outputs must not overlap inputs.

@@ -101,3 +101,14 @@ def test_window_backward_in_place_is_refused(out, other, shift):
         ctypes.byref(p.c()), at["q"], at["k"], at["v"], at["o"], at["lse"], at["d_o"], None, 128, 16, 4, at["dq"],
         at["dk"], at["dv"], at["ws"], 1 << 40, None)
     assert st == _lib.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("which", ["starts", "q_lens"])
+def test_norm_rope_lengths_in_place_are_refused(which):
+    # other CTAs still read them when the new lengths are written
+    p = ops.Params(2, 8, 2)
+    at = {n: (i + 1) << 24 for i, n in enumerate(("q", "k", "v", "table", "starts", "q_lens", "qo", "ko", "vo"))}
+    st = _lib.load().infllmv2_qk_norm_rope(
+        ctypes.byref(p.c()), at["q"], 1024, at["k"], 256, at["v"], 256, 4, None, None, 0, 1e-6, at["table"], 64, 128, 0,
+        at["starts"], at["q_lens"], at["qo"], at["ko"], at["vo"], 64, 1, at[which], None)
+    assert st == _lib.ERR_INVALID_ARG

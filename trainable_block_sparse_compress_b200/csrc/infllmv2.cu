@@ -1285,7 +1285,7 @@ int infllmv2_qk_norm_rope(const infllmv2_params* p, const void* q, int64_t q_str
   if (st != INFLLMV2_OK) return st;
   if ((st = check_len(Lout)) != INFLLMV2_OK) return st;
   if (!v || !q_out || !k_out || !v_out || !aligned16(v) || !aligned16(q_out) || !aligned16(k_out) ||
-      !aligned16(v_out) || !aligned4(lens_out) || (lens_out != nullptr && lens_out == starts))
+      !aligned16(v_out) || !aligned4(lens_out) || (lens_out != nullptr && (lens_out == starts || lens_out == q_lens)))
     return INFLLMV2_ERR_INVALID_ARG;
   if (v_stride < static_cast<int64_t>(p->num_kv_heads) * kHeadDim || v_stride % 8 != 0) return INFLLMV2_ERR_INVALID_ARG;
   if ((at_position != 0 && at_position != 1) || (at_position == 0 && Lout < Lq)) return INFLLMV2_ERR_INVALID_ARG;
