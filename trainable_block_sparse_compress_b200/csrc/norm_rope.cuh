@@ -6,7 +6,8 @@
 //   (y_a, y_b) <- (y_a c_i - y_b s_i, y_a s_i + y_b c_i) for the pairs of the first rot dims.
 // Backward, with g = R(-t) dy (the rotation is orthogonal up to the table's scale, and its
 // transpose is the rotation by -t with the same scale):
-//   d_w = sum over rows of g x r,   dx = r (g w) - x r^3 mean(g w x).
+//   d_w = sum over rows of g x r,   dx = r (g w) - x r^3 mean(g w x)
+// (formed as r (g w - (x r) r mean(g w x)): r^3 leaves fp32's range before dx does).
 // Everything is fp32 in registers, rounded once to bf16 on the way out.
 //
 // Both passes are bound by HBM: each head row is read once and written once (256 bytes each
@@ -16,12 +17,13 @@
 // of one token (all queries, or keys and values), so the token's row of the table and one
 // weight vector stay in registers, with kNrRows rows in flight; the arithmetic is packed in
 // pairs (f32x2), since with one value an instruction the issue slots, not HBM, would bound it.
-// Measured on a 128K prompt, 32 / 2 heads, 2.48 GB: 412 us (0.92 of the measured copy bandwidth);
-// 12 heads an item 442, six rows in flight at two CTAs an SM 526, one wave of CTAs (the short key
-// and value items then leave their SMs early) 477 to 806.
+// Measured on a 128K prompt, 32 / 2 heads, 2.48 GB: 453 us a call on changing inputs (0.83 of the
+// measured copy bandwidth), 412 us (0.92) repeated on one; against that, 12 heads an item 442, six
+// rows in flight at two CTAs an SM 526, one wave of CTAs (the short key and value items then leave
+// their SMs early) 477 to 806.
 // The backward copies a lane's values into its own slots of shared memory, kNrBwdRows rows ahead
 // of the ones it works on: rows in flight cost no registers.  One wave of CTAs, dealt to the query
-// and to the key and value heads by their bytes.  Measured, 2 x 8191 tokens, 453 MB: 92 us (0.75; 0.85
+// and to the key and value heads by their bytes.  Measured, 2 x 8191 tokens, 453 MB: 94 us a call (0.73; 0.85
 // at 65536 tokens); rows loaded into registers 112, as many CTAs for each chunk of heads 103, two
 // rows ahead 100, eight rows with 12 warps an SM 120, one row's dependent chain at a time 94.
 #pragma once

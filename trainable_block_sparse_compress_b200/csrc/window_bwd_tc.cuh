@@ -21,7 +21,7 @@
 //
 // Bound by the tensor pipe (70 % busy) and, in long runs, the power cap.  Measured, 32768 tokens,
 // 32 / 2 heads, W 4096, 64 sinks: 5.6 ms (0.94 PFLOP/s of the algorithmic 5 products, 1.3 of the 7),
-// 6.1 to 6.4 ms back to back.  Two elementwise warpgroups of 64 columns each instead of four: 10 ms.
+// 6.4 to 6.5 ms a call back to back.  Two elementwise warpgroups of 64 columns each instead of four: 10 ms.
 #pragma once
 #include "common.cuh"
 #include "tcgen05.cuh"

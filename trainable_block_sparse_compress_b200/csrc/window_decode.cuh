@@ -11,8 +11,9 @@
 // chunk ends.  A (sequence, kv-head) that is one chunk writes its output directly; up to 16 chunks
 // are a thread-block cluster and joined through distributed shared memory (one launch, no round
 // trip through HBM); more are joined by window_decode_merge_kernel through the workspace.
-// Measured: 32 ragged 128K sequences, 32 / 2 heads, every key: 452 us, 7.1 TB/s; 8 sequences, W 4096:
-// 12.3 us in one cluster launch, 13.1 us with the join through the workspace (cold L2: 20.5, 21.5).
+// Measured: 32 ragged 128K sequences, 32 / 2 heads, every key: 465 us a call, 6.9 TB/s (452 repeated);
+// 8 sequences, W 4096, on the GPU: 12.3 us in one cluster launch, 13.1 us with the join through the
+// workspace (cold L2: 20.5, 21.5); 15.7 us a call.
 #pragma once
 #include <cooperative_groups.h>
 

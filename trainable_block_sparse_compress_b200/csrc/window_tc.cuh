@@ -23,7 +23,8 @@
 //
 // Bound by the chain of a tile: scores, softmax (~2100 cycles), P V and the next scores (~1100);
 // the tensor pipe is busy 55 % of the time.  Measured: 128K prompt, 32 / 2 heads, W 4096: 1.17 PFLOP/s
-// (7.5 ms; 8.5 ms back to back, under the power cap); 2 x 8191 tokens, 32 / 8 heads, causal: 0.94 ms.
+// (7.5 ms; 8.7 ms a call back to back, under the power cap); 2 x 8191 tokens, 32 / 8 heads, causal:
+// 0.94 ms (1.1 ms a call).
 // 64-key tiles with two score buffers (no chain, but a 64-wide product takes 59 of a 128-wide one's
 // 64 cycles) 11.2 ms; two threads a row 8.7.
 #pragma once
