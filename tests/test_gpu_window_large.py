@@ -220,3 +220,23 @@ def test_a_workspace_with_gaps_is_refused():
     for n in (1, 1 << 26):  # one too small is replaced
         got = ops.window_attn_chunk(p, q, k, v, 100000, ws=torch.empty(n, dtype=torch.uint8, device="cuda"))
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_longest_sequence_forward_and_backward():
+    """The last tokens of 262144: they see the last keys only, so a slice of them is the whole reference."""
+    L, Hq, Hkv, W, n = 262144, 4, 2, 300, 500
+    q, k, v = inputs(1, L, L, Hq, Hkv, seed=9)
+    do = randn(torch.Generator(device="cuda").manual_seed(10), 1, L, Hq, 128)
+    p = ops.Params(1, Hq, Hkv)
+    o, lse = ops.window_attn_prefill(p, q, k, v, W)
+    dq, dk, dv = ops.window_attn_backward(p, q, k, v, o, lse, do, W)
+    m = n + W  # tokens of the slice; its last n have all of their keys and queries in it
+    qs, os_, ds = (x[0, -m:] for x in (q, o, do))
+    ks, vs, ls = k[0, :, -m:], v[0, :, -m:], lse[0, :, -m:]
+    w, z, tw, tz = attend(qs, ks, vs, 0, W, 0)
+    close(o[0, -n:], w[-n:], tw[-n:], "o")
+    close(lse[0, :, -n:], z[:, -n:], tz[:, -n:], "lse")
+    ref, tol = attend_backward(qs, ks, vs, os_, ls, ds, W, 0)
+    close(dq[0, -n:], ref[0][-n:], tol[0][-n:], "dq")
+    for got, r, t, name in ((dk, ref[1], tol[1], "dk"), (dv, ref[2], tol[2], "dv")):
+        close(got[0, :, -n:], r[:, -n:], t[:, -n:], name)
